@@ -13,6 +13,10 @@ bundles them with the buffers of one geometry.
 import ctypes
 import os
 
+from . import block
+from .block import (MoELayerW4, MoeNorm, MoeRouter, MoeW4Geom, make_router, make_w4_geom,  # noqa: F401
+                    moe_add_rmsnorm, moe_add_rmsnorm_backward, moe_add_rmsnorm_workspace_size,
+                    moe_forward_w4_workspace_size, moe_quantize_w4, moe_route_topk, moe_route_topk_backward)
 from .build import LIB_PATH, build  # noqa: F401
 
 LAYOUT = {"EM": 0, "RM": 1, "FLAT": 2}
@@ -92,6 +96,7 @@ def lib():
                   "moe_forward_host", "moe_quantize_weights_fp8", "moe_prepare_weights_fp8",
                   "moe_expert_ffn_fp8"):
             getattr(L, f).restype = ctypes.c_int
+        block.bind(L)
         _lib = L
     return _lib
 
