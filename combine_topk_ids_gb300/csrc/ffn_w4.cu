@@ -6,17 +6,23 @@
 //
 // A decode batch has few rows for each expert, so the time is that of reading the picked
 // experts' codes once.  They feed warp-level matrix instructions (16 weight rows x 16 inputs
-// x 8 batch rows, bf16 with float32 sums) straight from global memory: the prepared order
-// gives each lane the 32 weights of its matrix fragments for 64 inputs in one 16-byte load,
-// 512 contiguous bytes for the warp.  Codes become bf16 integers without rounding; the sums
-// over a group of inputs are multiplied by its scale in float32.
+// x 8 batch rows, bf16 with float32 sums): a tcgen05 tile of 128 rows would be nearly empty,
+// and its operands would have to be unpacked into shared memory first.  Codes become bf16
+// integers without rounding; the sums over a group of inputs are multiplied by its scale in
+// float32.  A block takes eight tiles of 16 weight rows; for 128 inputs at a time one warp
+// copies their codes and scales (contiguous in the prepared order) and the batch rows' inputs
+// to a ring of stages in shared memory, and four warps compute two tiles each.
 #include "block_common.cuh"
+#include "tc_common.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kW4Warps = 8;
-constexpr int kAhead = 8;      // 16-byte weight loads that a lane has under way
+constexpr int kW4Tiles = 8;    // tiles of 16 weight rows that a block takes at a time
+constexpr int kW4Warps = 4;    // computing warps, two tiles each; one more warp copies
+constexpr int kW4Threads = (kW4Warps + 1) * 32;
+constexpr int kW4Blocks = 4;   // blocks on an SM
+constexpr int kW4Cols = 16;    // columns of inputs at a time
 
 struct W4Plan {
     int64_t T, H, E, k, I, P, G;
@@ -105,95 +111,114 @@ __global__ void __launch_bounds__(1024) w4_group_kernel(W4Args a) {
     }
 }
 
-__device__ __forceinline__ uint4 ld_stream(const uint4 *p) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-}
-
+// c (+)= a b; ZERO: the sum starts here.
+template <bool ZERO>
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    if (ZERO)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+            : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Eight codes (nibble i + 4j: element j of fragment register i) to four bf16 pairs of
-// code - 8: a code in the low mantissa bits of 128 is 128 + code, and 136 is taken off again.
-__device__ __forceinline__ void unpack_codes(uint32_t w, uint32_t (&a)[4]) {
-    const __nv_bfloat162 off = __float2bfloat162_rn(136.f);
+// One matrix step of 16 inputs for NT blocks of columns: eight codes (nibble i + 4j: element j
+// of fragment register i) times b.  A code in the low mantissa bits of 128 is the bf16 number
+// 128 + code; 136 is taken off again, exactly.
+template <bool ZERO, int NT>
+__device__ __forceinline__ void w4_step(float (&part)[NT][4], uint32_t w, const uint32_t (&b0)[NT],
+                                        const uint32_t (&b1)[NT]) {
+    uint32_t f[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t v = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
-        const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&v), off);
-        a[i] = *reinterpret_cast<const uint32_t *>(&d);
+        uint32_t v;   // (w >> 4i) & 0x000f000f | 0x43004300
+        asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(v) : "r"(w >> (4 * i)), "r"(0x000f000fu), "r"(0x43004300u));
+        const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&v), __float2bfloat162_rn(136.f));
+        f[i] = *reinterpret_cast<const uint32_t *>(&d);
     }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) mma_bf16<ZERO>(part[n], f, b0[n], b1[n]);
 }
 
-// acc[n][.] = one tile of 16 weight rows times NT blocks of 8 columns, over K inputs.
-//   w       the tile's prepared codes, at this lane's 16 bytes of the first 64 inputs
-//   sc      the tile's prepared scales, at this lane's first pair (rows g, g + 8)
-//   col[n]  this lane's column (lane / 4 of block n) of inputs, or NULL (a column of zeros)
+// What a block works on at a time: kW4Tiles tiles of one expert for up to 16 columns of its
+// picks (PER columns a pick).  Walks the units (expert, tiles) of the call from block to block.
+template <int PER>
+struct W4Item {
+    int64_t u, group;
+    int i, begin, end;   // group of tiles within the expert; the picks a.rows[begin .. end) still to do
+
+    __device__ __forceinline__ int picks() const { return min(end - begin, kW4Cols / PER); }
+    __device__ __forceinline__ bool start(const W4Args &a, int groups, int64_t units) {
+        if (u >= units) return false;
+        const int which = (int)(u / groups);
+        const int32_t *ids = a.head + 1, *starts = a.head + 1 + a.E;
+        i = (int)(u - (int64_t)which * groups);
+        group = (int64_t)ids[which] * groups + i;
+        begin = starts[which];
+        end = starts[which + 1];
+        return true;
+    }
+    __device__ __forceinline__ bool advance(const W4Args &a, int groups, int64_t units) {
+        begin += picks();
+        if (begin < end) return true;
+        u += gridDim.x;
+        return start(a, groups, units);
+    }
+};
+
+// A stage holds 128 inputs: the tiles' codes and scales, and the columns' inputs.  The columns
+// lie 64 bytes more apart than they are long, so that the eight lanes of a shared-memory phase
+// (two columns, four 16-byte pieces) fall on different banks.
+template <int G>
+struct W4Stage {
+    static constexpr int kPairs = 128 / G;   // scale pairs (rows g, g + 8) per 128 inputs
+    static constexpr int kCodes = kW4Tiles * 1024, kScales = kW4Tiles * 32 * kPairs, kColumn = 256 + 64;
+    static constexpr int kBytes = kCodes + kScales + kW4Cols * kColumn;
+    static constexpr int kStages = G == 32 ? 3 : 4;   // what fits four blocks of an SM
+};
+
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+// One stage for the warp's two tiles: acc[t][n][.] += tile t times column block n.
 template <int NT, int G>
-__device__ __forceinline__ void w4_tile(const uint4 *w, const uint16_t *sc, const uint16_t *const (&col)[NT], int K,
-                                        float (&acc)[NT][4]) {
-    constexpr int kPairs = 128 / G;   // scale pairs per 128 inputs
-    const int q = threadIdx.x & 3;
-    const int chunks = K / 64;
-    uint4 buf[kAhead];
+__device__ __forceinline__ void w4_compute(const uint8_t *stage, int warp, float (&acc)[2][NT][4]) {
+    using S = W4Stage<G>;
+    constexpr int kPairs = S::kPairs;
+    const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+    const uint4 *w = reinterpret_cast<const uint4 *>(stage) + warp * 2 * 64 + lane;
+    const uint32_t *sc = reinterpret_cast<const uint32_t *>(stage + S::kCodes) + (warp * 2 * 8 + g) * kPairs;
+    const uint8_t *x = stage + S::kCodes + S::kScales + g * S::kColumn + q * 16;
+    float part[2][NT][4];
+    uint4 v[2];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-        buf[i] = i < chunks ? ld_stream(w + (int64_t)i * 32) : make_uint4(0, 0, 0, 0);
+    for (int h = 0; h < 4; ++h) {   // 32 inputs: two matrix steps
+        uint32_t b0[NT], b1[NT], b2[NT], b3[NT];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n) {
+            const uint4 b = *reinterpret_cast<const uint4 *>(x + n * 8 * S::kColumn + h * 64);
+            b0[n] = b.x; b1[n] = b.y; b2[n] = b.z; b3[n] = b.w;
+        }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
-    for (int c0 = 0; c0 < chunks; c0 += kAhead) {
+        for (int t = 0; t < 2; ++t) {
+            if (h % 2 == 0) v[t] = w[t * 64 + h / 2 * 32];
+            if (h * 32 % G == 0) w4_step<true, NT>(part[t], h % 2 ? v[t].z : v[t].x, b0, b1);
+            else w4_step<false, NT>(part[t], h % 2 ? v[t].z : v[t].x, b0, b1);
+            w4_step<false, NT>(part[t], h % 2 ? v[t].w : v[t].y, b2, b3);
+            if ((h + 1) * 32 % G == 0) {
+                const uint32_t p = sc[t * 8 * kPairs + h * 32 / G];
 #pragma unroll
-        for (int u = 0; u < kAhead; u += 2) {
-            if (c0 + u < chunks) {   // chunks is even: 128 inputs at a time
-                uint32_t pairs[kPairs];
-#pragma unroll
-                for (int i = 0; i < kPairs; ++i)
-                    pairs[i] = __ldg(reinterpret_cast<const uint32_t *>(sc) + (int64_t)(c0 + u) / 2 * 8 * kPairs + i);
-                float part[NT][4];
-#pragma unroll
-                for (int step = 0; step < 8; step += 2) {   // 32 inputs: two matrix steps
-                    const uint4 v = buf[u + step / 4];
-                    uint4 b[NT];
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        b[n] = col[n] ? __ldg(reinterpret_cast<const uint4 *>(col[n] + (c0 + u) * 64 + step * 16 + q * 8))
-                                      : make_uint4(0, 0, 0, 0);
-                    if (step * 16 % G == 0) {
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) part[n][i] = 0.f;
-                    }
-                    uint32_t f[4];
-                    unpack_codes(step % 4 == 0 ? v.x : v.z, f);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) mma_bf16(part[n], f, b[n].x, b[n].y);
-                    unpack_codes(step % 4 == 0 ? v.y : v.w, f);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) mma_bf16(part[n], f, b[n].z, b[n].w);
-                    if ((step + 2) * 16 % G == 0) {
-                        const uint32_t p = pairs[step * 16 / G];
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            acc[n][0] = fmaf(lo_f32(p), part[n][0], acc[n][0]);
-                            acc[n][1] = fmaf(lo_f32(p), part[n][1], acc[n][1]);
-                            acc[n][2] = fmaf(hi_f32(p), part[n][2], acc[n][2]);
-                            acc[n][3] = fmaf(hi_f32(p), part[n][3], acc[n][3]);
-                        }
-                    }
+                for (int n = 0; n < NT; ++n) {
+                    acc[t][n][0] = fmaf(lo_f32(p), part[t][n][0], acc[t][n][0]);
+                    acc[t][n][1] = fmaf(lo_f32(p), part[t][n][1], acc[t][n][1]);
+                    acc[t][n][2] = fmaf(hi_f32(p), part[t][n][2], acc[t][n][2]);
+                    acc[t][n][3] = fmaf(hi_f32(p), part[t][n][3], acc[t][n][3]);
                 }
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    if (c0 + u + i + kAhead < chunks) buf[u + i] = ld_stream(w + (int64_t)(c0 + u + i + kAhead) * 32);
             }
         }
     }
@@ -201,19 +226,12 @@ __device__ __forceinline__ void w4_tile(const uint4 *w, const uint16_t *sc, cons
 
 __device__ __forceinline__ float silu(float v) { return __fdiv_rn(v, 1.0f + expf(-v)); }
 
-// Gate and up rows i0 .. i0 + 7 of one expert (they share a tile: rows 0..7 and 8..15) for up
-// to 8 NT of its picks.
-template <int NT, int G>
-__device__ __forceinline__ void w4_up(const W4Args &a, int64_t tile, int i0, const int32_t *rows, int n) {
+// First product: a tile is rows i0 .. i0 + 7 of the gate and of the up matrix (its rows 0..7
+// and 8..15), so a lane holds both factors of its activations.
+template <int NT>
+__device__ __forceinline__ void w4_store_act(const W4Args &a, int i0, const int32_t *rows, int n,
+                                             const float (&acc)[NT][4]) {
     const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-    const uint16_t *col[NT];
-#pragma unroll
-    for (int b = 0; b < NT; ++b) {
-        const int c = 8 * b + g;
-        col[b] = c < n ? a.x + (int64_t)(rows[c] / a.k) * a.H : nullptr;
-    }
-    float acc[NT][4];
-    w4_tile<NT, G>(a.w1 + tile * (a.H / 64) * 32 + lane, a.s1 + (tile * (a.H / G) * 8 + g * (128 / G)) * 2, col, a.H, acc);
 #pragma unroll
     for (int b = 0; b < NT; ++b)
 #pragma unroll
@@ -230,19 +248,12 @@ __device__ __forceinline__ void w4_up(const W4Args &a, int64_t tile, int i0, con
         }
 }
 
-// Output rows h0 .. h0 + 15 for up to 4 NT picks: columns 2r and 2r + 1 are the high and the
-// low part of pick r's activation, whose products are added at the end.
-template <int NT, int G>
-__device__ __forceinline__ void w4_down(const W4Args &a, int64_t tile, int h0, const int32_t *rows, int n) {
+// Second product: columns 2r and 2r + 1 are the high and the low part of pick r's activation,
+// whose products are added here.
+template <int NT>
+__device__ __forceinline__ void w4_store_y(const W4Args &a, int h0, const int32_t *rows, int n,
+                                           const float (&acc)[NT][4]) {
     const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-    const uint16_t *col[NT];
-#pragma unroll
-    for (int b = 0; b < NT; ++b) {
-        const int c = 8 * b + g;
-        col[b] = c / 2 < n ? a.act + ((int64_t)rows[c / 2] * 2 + (c & 1)) * a.I : nullptr;
-    }
-    float acc[NT][4];
-    w4_tile<NT, G>(a.w2 + tile * (a.I / 64) * 32 + lane, a.s2 + (tile * (a.I / G) * 8 + g * (128 / G)) * 2, col, a.I, acc);
 #pragma unroll
     for (int b = 0; b < NT; ++b) {
         const int r = 4 * b + q;
@@ -253,33 +264,109 @@ __device__ __forceinline__ void w4_down(const W4Args &a, int64_t tile, int h0, c
     }
 }
 
-// UP: the first product and the activation; else the second product.  A warp takes a tile of
-// one expert at a time; the warps of a block take neighbouring tiles and so share inputs.
+// UP: the first product and the activation; else the second product.
 template <bool UP, int G>
-__global__ void __launch_bounds__(kW4Warps * 32, 2) w4_product_kernel(W4Args a) {
-    pdl_begin();
-    const int tiles = UP ? a.I / 8 : a.H / 16;
-    const int64_t units = (int64_t)a.head[0] * tiles;
-    const int32_t *ids = a.head + 1, *starts = a.head + 1 + a.E;
-    const int64_t stride = (int64_t)gridDim.x * kW4Warps;
-    for (int64_t u = (int64_t)blockIdx.x * kW4Warps + (threadIdx.x >> 5); u < units; u += stride) {
-        const int which = (int)(u / tiles), i = (int)(u - (int64_t)which * tiles);
-        const int64_t tile = (int64_t)ids[which] * tiles + i;
-        const int begin = starts[which], end = starts[which + 1];
-        const int per = UP ? 1 : 2;   // columns per row
-        for (int r = begin; r < end;) {
-            const int left = end - r;
-            if (left * per <= 8) {
-                if (UP) w4_up<1, G>(a, tile, 8 * i, a.rows + r, left);
-                else w4_down<1, G>(a, tile, 16 * i, a.rows + r, left);
-                break;
-            }
-            const int n = min(left, 16 / per);
-            if (UP) w4_up<2, G>(a, tile, 8 * i, a.rows + r, n);
-            else w4_down<2, G>(a, tile, 16 * i, a.rows + r, n);
-            r += n;
+__global__ void __launch_bounds__(kW4Threads, kW4Blocks) w4_product_kernel(W4Args a) {
+    using S = W4Stage<G>;
+    extern __shared__ __align__(128) uint8_t stages[];   // [kStages][kBytes]
+    __shared__ __align__(8) uint64_t full[S::kStages], empty[S::kStages];
+    __shared__ int abort_flag;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        abort_flag = 0;
+        for (int i = 0; i < S::kStages; ++i) {
+            mbar_init(smem_u32(full + i), 1);
+            mbar_init(smem_u32(empty + i), kW4Warps);
         }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    __syncthreads();
+    pdl_begin();
+    const int K = UP ? a.H : a.I, blocks = K / 128;
+    const int groups = (UP ? a.I / 8 : a.H / 16) / kW4Tiles;
+    const int64_t units = (int64_t)a.head[0] * groups;
+    constexpr int kPer = UP ? 1 : 2;
+    W4Item<kPer> it;
+    it.u = blockIdx.x;
+    if (!it.start(a, groups, units)) return;
+    int stage = 0;
+    uint32_t phase = 0;
+    auto next_stage = [&] {
+        if (++stage == S::kStages) {
+            stage = 0;
+            phase ^= 1;
+        }
+    };
+
+    if (warp == kW4Warps) {   // the copying warp: lanes 0..15 a column each, 16 codes, 17 scales
+        int put = 0;
+        bool ok = true;
+        do {
+            const int n = it.picks() * kPer;
+            const char *src = nullptr;
+            uint32_t bytes = 0, off = 0;
+            int step = 0;
+            if (lane < n) {
+                const int64_t p = a.rows[it.begin + lane / kPer];
+                src = reinterpret_cast<const char *>(UP ? a.x + p / a.k * a.H : a.act + (p * 2 + (lane & 1)) * a.I);
+                bytes = step = 256;
+                off = S::kCodes + S::kScales + lane * S::kColumn;
+            } else if (lane == 16) {
+                src = reinterpret_cast<const char *>(UP ? a.w1 : a.w2) + it.group * blocks * S::kCodes;
+                bytes = step = S::kCodes;
+            } else if (lane == 17) {
+                src = reinterpret_cast<const char *>(UP ? a.s1 : a.s2) + it.group * blocks * S::kScales;
+                bytes = step = S::kScales;
+                off = S::kCodes;
+            }
+            for (int b = 0; b < blocks; ++b) {
+                ok = mbar_wait(smem_u32(empty + stage), phase ^ 1, &abort_flag, a.status);
+                ok = __all_sync(kAllLanes, ok);
+                if (!ok) break;
+                if (lane == 0) mbar_expect_tx(smem_u32(full + stage), S::kCodes + S::kScales + n * 256);
+                __syncwarp();
+                if (bytes) bulk_copy(smem_u32(stages) + stage * S::kBytes + off, src, bytes, smem_u32(full + stage));
+                src += step;
+                ++put;
+                next_stage();
+            }
+        } while (ok && it.advance(a, groups, units));
+        if (!ok) {
+            // gave up: the copies under way may not outlive the block, so each stage's gets one
+            // more bounded wait (the status word already holds MOE_STATUS_TIMEOUT)
+            for (int i = max(0, put - S::kStages); i < put; ++i) {
+                const unsigned long long t0 = globaltimer();
+                while (!mbar_try_wait(smem_u32(full + i % S::kStages), i / S::kStages & 1) &&
+                       globaltimer() - t0 < kWaitLimitNs) {}
+            }
+        }
+        return;
+    }
+
+    do {
+        const int32_t *rows = a.rows + it.begin;
+        const int n = it.picks();
+        const int first = (it.i * kW4Tiles + warp * 2) * (UP ? 8 : 16);   // of the warp's first tile
+        auto run = [&](auto blocks_of_columns) {
+            constexpr int NT = decltype(blocks_of_columns)::value;
+            float acc[2][NT][4] = {};
+            for (int b = 0; b < blocks; ++b) {
+                const bool in = mbar_wait(smem_u32(full + stage), phase, &abort_flag, a.status);
+                if (!__all_sync(kAllLanes, in)) return false;
+                w4_compute<NT, G>(stages + stage * S::kBytes, warp, acc);
+                __syncwarp();   // every lane has read the stage
+                if (lane == 0) mbar_arrive(smem_u32(empty + stage));
+                next_stage();
+            }
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if constexpr (UP) w4_store_act<NT>(a, first + 8 * t, rows, n, acc[t]);
+                else w4_store_y<NT>(a, first + 16 * t, rows, n, acc[t]);
+            }
+            return true;
+        };
+        if (!(n * kPer <= 8 ? run(std::integral_constant<int, 1>{}) : run(std::integral_constant<int, 2>{}))) return;
+    } while (it.advance(a, groups, units));
 }
 
 // out[t] = sum over the picks, in their order, of weight * y; eight columns per thread.
@@ -308,15 +395,16 @@ __global__ void __launch_bounds__(256) w4_combine_kernel(W4Args a) {
 // from k0 on, lane (g, q) of a tile holds rows g and g + 8, inputs k0 + 8q .. + 7 and
 // k0 + 32 + 8q .. + 7: word s (matrix step s) has nibble i + 4j = element j of fragment
 // register i, where registers 0, 2 are row g and 1, 3 row g + 8, and registers 2, 3 the next
-// two inputs.  One thread per lane and 64 inputs.
+// two inputs.  The order is [8 tiles][128 inputs][tile][64 inputs][lane]; one thread per lane
+// and 64 inputs.
 __global__ void __launch_bounds__(256) w4_order_codes_kernel(const uint8_t *codes, uint4 *out, int64_t n, int rows,
                                                              int K, int half) {
     const int64_t v = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (v >= n) return;
     const int lane = (int)(v & 31), g = lane >> 2, q = lane & 3;
-    const int64_t c = v >> 5;
-    const int chunk = (int)(c % (K / 64));
-    const int64_t tile = c / (K / 64);
+    const int64_t c = v / (64 * kW4Tiles);   // [8 tiles][128 inputs]
+    const int chunk = (int)(c % (K / 128)) * 2 + (int)(v >> 5 & 1);
+    const int64_t tile = c / (K / 128) * kW4Tiles + (v >> 6) % kW4Tiles;
     const int64_t e = tile / (rows / 16);
     const int i = (int)(tile - e * (rows / 16));
     const int64_t r0 = e * rows + (half ? 8 * i : 16 * i) + g, r1 = r0 + (half ? half : 8);
@@ -337,16 +425,16 @@ __global__ void __launch_bounds__(256) w4_order_codes_kernel(const uint8_t *code
     out[v] = make_uint4(word[0], word[1], word[2], word[3]);
 }
 
-// Scales in the order [tile][128 inputs][g][group][rows g, g + 8]; one thread per pair.
+// Scales in the order [8 tiles][128 inputs][tile][g][group][rows g, g + 8]; one thread per pair.
 __global__ void __launch_bounds__(256) w4_order_scales_kernel(const uint16_t *scales, uint32_t *out, int64_t n,
                                                               int rows, int K, int half, int G) {
     const int64_t v = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (v >= n) return;
     const int per = 128 / G;
     const int j = (int)(v % per), g = (int)(v / per % 8);
-    const int64_t c = v / (8 * per);
+    const int64_t c = v / (8 * per * kW4Tiles);
     const int block = (int)(c % (K / 128));
-    const int64_t tile = c / (K / 128);
+    const int64_t tile = c / (K / 128) * kW4Tiles + v / (8 * per) % kW4Tiles;
     const int64_t e = tile / (rows / 16);
     const int i = (int)(tile - e * (rows / 16));
     const int64_t r0 = e * rows + (half ? 8 * i : 16 * i) + g, r1 = r0 + (half ? half : 8);
@@ -410,15 +498,27 @@ cudaError_t order_matrix(const uint8_t *codes, const void *scales, uint8_t *out,
     return cudaGetLastError();
 }
 
+template <bool UP, int G>
+cudaError_t launch_product_of(const W4Args &a, unsigned blocks, cudaStream_t s) {
+    constexpr int smem = W4Stage<G>::kStages * W4Stage<G>::kBytes;
+    static std::once_flag once[64];   // per device
+    static cudaError_t set[64];
+    const int dev = device_ordinal();
+    if (dev < 0) return cudaErrorInvalidDevice;
+    std::call_once(once[dev], [&] {
+        set[dev] = cudaFuncSetAttribute(w4_product_kernel<UP, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    });
+    if (set[dev] != cudaSuccess) return set[dev];
+    return launch_pdl(w4_product_kernel<UP, G>, dim3(blocks), dim3(kW4Threads), smem, s, a);
+}
+
 template <bool UP>
 cudaError_t launch_product(const W4Args &a, int64_t G, int64_t most_units, cudaStream_t s) {
-    int64_t blocks = (most_units + kW4Warps - 1) / kW4Warps;
-    const int64_t most = 2 * (int64_t)num_sms();
-    if (blocks > most) blocks = most;
-    const dim3 grid((unsigned)blocks), block(kW4Warps * 32);
-    if (G == 32) return launch_pdl(w4_product_kernel<UP, 32>, grid, block, 0, s, a);
-    if (G == 64) return launch_pdl(w4_product_kernel<UP, 64>, grid, block, 0, s, a);
-    return launch_pdl(w4_product_kernel<UP, 128>, grid, block, 0, s, a);
+    const int64_t most = kW4Blocks * (int64_t)num_sms();
+    const unsigned blocks = (unsigned)(most_units < most ? most_units : most);
+    if (G == 32) return launch_product_of<UP, 32>(a, blocks, s);
+    if (G == 64) return launch_product_of<UP, 64>(a, blocks, s);
+    return launch_product_of<UP, 128>(a, blocks, s);
 }
 
 }  // namespace
@@ -511,8 +611,8 @@ int moe_forward_w4(const moe_w4_geom *g, const void *x_dev, const void *topk_ids
     cudaError_t e = launch_pdl(w4_group_kernel, dim3(1), dim3(1024), 0, s, a);
     if (e == cudaSuccess && p.T > 0) {
         const int64_t used = p.P < p.E ? p.P : p.E;   // experts that can have picks
-        e = launch_product<true>(a, p.G, used * (p.I / 8), s);
-        if (e == cudaSuccess) e = launch_product<false>(a, p.G, used * (p.H / 16), s);
+        e = launch_product<true>(a, p.G, used * (p.I / 8 / kW4Tiles), s);
+        if (e == cudaSuccess) e = launch_product<false>(a, p.G, used * (p.H / 16 / kW4Tiles), s);
         if (e == cudaSuccess)
             e = launch_pdl(w4_combine_kernel, dim3(blocks256(p.T * (p.H / 8))), dim3(256), 0, s, a);
     }

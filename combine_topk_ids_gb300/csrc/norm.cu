@@ -25,55 +25,64 @@ struct NormArgs {
     unsigned shift_mask;      // 15: chunks follow the 16-byte boundaries of x's rows; 0: columns
 };
 
-// Elements [i, i + 8) of a row as float32; those outside [0, H) are 0 and are not read.
-// One 16-byte load (two for float32) where the address allows it.
+// Columns [i, i + 8) of a row, in the row's own type.  load() issues one 16-byte load (two for
+// float32) where they all exist and the address allows it, and nothing else, so that a
+// thread's loads are under way together; floats() fetches what load() could not: the columns
+// of [0, H) one by one, 0 outside.
 template <bool F32>
-__device__ __forceinline__ void load8(const void *row, int i, int H, float (&f)[8]) {
-    if (F32) {
-        const float *p = static_cast<const float *>(row) + i;
-        if (i >= 0 && i + 8 <= H && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
-            const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
-            f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-            f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = (i + j >= 0 && i + j < H) ? p[j] : 0.f;
-        }
-    } else {
-        const __nv_bfloat16 *p = static_cast<const __nv_bfloat16 *>(row) + i;
-        if (i >= 0 && i + 8 <= H && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
-            const uint4 a = *reinterpret_cast<const uint4 *>(p);
-            f[0] = lo_f32(a.x); f[1] = hi_f32(a.x); f[2] = lo_f32(a.y); f[3] = hi_f32(a.y);
-            f[4] = lo_f32(a.z); f[5] = hi_f32(a.z); f[6] = lo_f32(a.w); f[7] = hi_f32(a.w);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = (i + j >= 0 && i + j < H) ? __bfloat162float(p[j]) : 0.f;
+struct Raw8 {
+    uint4 v[F32 ? 2 : 1];
+
+    static __device__ __forceinline__ bool whole(const void *row, int i, int H) {
+        return i >= 0 && i + 8 <= H && ((reinterpret_cast<uintptr_t>(row) + (int64_t)i * (F32 ? 4 : 2)) & 15) == 0;
+    }
+    __device__ __forceinline__ void load(const void *row, int i, int H) {
+        if (whole(row, i, H)) {
+            const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const char *>(row) + (int64_t)i * (F32 ? 4 : 2));
+            v[0] = p[0];
+            if (F32) v[F32 ? 1 : 0] = p[1];
         }
     }
-}
+    __device__ __forceinline__ void floats(const void *row, int i, int H, float (&f)[8]) const {
+        if (F32) {
+            const uint4 &a = v[0], &b = v[F32 ? 1 : 0];
+            f[0] = __uint_as_float(a.x); f[1] = __uint_as_float(a.y); f[2] = __uint_as_float(a.z); f[3] = __uint_as_float(a.w);
+            f[4] = __uint_as_float(b.x); f[5] = __uint_as_float(b.y); f[6] = __uint_as_float(b.z); f[7] = __uint_as_float(b.w);
+        } else {
+            const uint4 &a = v[0];
+            f[0] = lo_f32(a.x); f[1] = hi_f32(a.x); f[2] = lo_f32(a.y); f[3] = hi_f32(a.y);
+            f[4] = lo_f32(a.z); f[5] = hi_f32(a.z); f[6] = lo_f32(a.w); f[7] = hi_f32(a.w);
+        }
+        if (!whole(row, i, H)) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                f[j] = 0.f;
+                if (i + j >= 0 && i + j < H)
+                    f[j] = F32 ? static_cast<const float *>(row)[i + j]
+                               : __bfloat162float(static_cast<const __nv_bfloat16 *>(row)[i + j]);
+            }
+        }
+    }
+};
 
 template <bool F32>
 __device__ __forceinline__ void store8(void *row, int i, int H, const float (&f)[8]) {
-    if (F32) {
-        float *p = static_cast<float *>(row) + i;
-        if (i >= 0 && i + 8 <= H && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+    if (Raw8<F32>::whole(row, i, H)) {
+        if (F32) {
+            float *p = static_cast<float *>(row) + i;
             *reinterpret_cast<float4 *>(p) = make_float4(f[0], f[1], f[2], f[3]);
             *reinterpret_cast<float4 *>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
         } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (i + j >= 0 && i + j < H) p[j] = f[j];
+            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(row) + i) =
+                make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
         }
     } else {
-        __nv_bfloat16 *p = static_cast<__nv_bfloat16 *>(row) + i;
-        if (i >= 0 && i + 8 <= H && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
-            *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]),
-                                                       pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
-        } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (i + j >= 0 && i + j < H) p[j] = __float2bfloat16_rn(f[j]);
-        }
+        for (int j = 0; j < 8; ++j)
+            if (i + j >= 0 && i + j < H) {
+                if (F32) static_cast<float *>(row)[i + j] = f[j];
+                else static_cast<__nv_bfloat16 *>(row)[i + j] = __float2bfloat16_rn(f[j]);
+            }
     }
 }
 
@@ -123,15 +132,26 @@ __global__ void __launch_bounds__(MAXT) add_rmsnorm_kernel(NormArgs a) {
     const __nv_bfloat16 *x = static_cast<const __nv_bfloat16 *>(a.x) + tr * a.xs;
     const char *res = a.res ? static_cast<const char *>(a.res) + tr * a.rs * (R32 ? 4 : 2) : nullptr;
     const int s = (int)((reinterpret_cast<uintptr_t>(x) & a.shift_mask) >> 1);
+    Raw8<false> rx[VPT];
+    Raw8<R32> rr[VPT];
+    Raw8<W32> rw[VPT];
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+        const int i = 8 * (int)(threadIdx.x + v * blockDim.x) - s;
+        rx[v].load(x, i, H);
+        if (res) rr[v].load(res, i, H);
+    }
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) rw[v].load(a.w, 8 * (int)(threadIdx.x + v * blockDim.x) - s, H);
     float h[VPT][8];
     float ss = 0.f;
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
         const int i = 8 * (int)(threadIdx.x + v * blockDim.x) - s;
-        load8<false>(x, i, H, h[v]);
+        rx[v].floats(x, i, H, h[v]);
         if (res) {
             float r[8];
-            load8<R32>(res, i, H, r);
+            rr[v].floats(res, i, H, r);
 #pragma unroll
             for (int j = 0; j < 8; ++j) h[v][j] += r[j];
         }
@@ -146,7 +166,7 @@ __global__ void __launch_bounds__(MAXT) add_rmsnorm_kernel(NormArgs a) {
         const int i = 8 * (int)(threadIdx.x + v * blockDim.x) - s;
         if (a.sum) store8<R32>(static_cast<char *>(a.sum) + tr * a.ss * (R32 ? 4 : 2), i, H, h[v]);
         float w[8];
-        load8<W32>(a.w, i, H, w);
+        rw[v].floats(a.w, i, H, w);
         float y[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) y[j] = h[v][j] * rstd * w[j];
@@ -183,25 +203,44 @@ __global__ void __launch_bounds__(MAXT) add_rmsnorm_backward_kernel(NormBackArgs
     for (int v = 0; v < VPT; ++v)
 #pragma unroll
         for (int j = 0; j < 8; ++j) dw[v][j] = 0.f;
+    Raw8<W32> rw[VPT];
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) rw[v].load(a.w, 8 * (int)(threadIdx.x + v * blockDim.x), a.H);
+    Raw8<false> rg[VPT];
+    Raw8<R32> rh[VPT], rs[VPT];
+    float rstd = 0.f;
+    // row t's inputs under way, while the row before it is computed
+    auto fetch = [&](int64_t t) {
+        const int H = t < a.T ? a.H : 0;
+        const int64_t tr = t < a.T ? t : 0;
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            const int i = 8 * (int)(threadIdx.x + v * blockDim.x);
+            rg[v].load(static_cast<const __nv_bfloat16 *>(a.dout) + tr * a.ds, i, H);
+            rh[v].load(static_cast<const char *>(a.h) + tr * a.hs * (R32 ? 4 : 2), i, H);
+            if (a.dsum) rs[v].load(static_cast<const char *>(a.dsum) + tr * a.ss * (R32 ? 4 : 2), i, H);
+        }
+        rstd = t < a.T ? a.rstd[t] : 0.f;
+    };
     const int64_t groups = ((int64_t)a.T + blockDim.y - 1) / blockDim.y;
+    fetch((int64_t)blockIdx.x * blockDim.y + threadIdx.y);
     for (int64_t gr = blockIdx.x; gr < groups; gr += gridDim.x) {
         const int64_t t = gr * blockDim.y + threadIdx.y;
-        const bool live = t < a.T;
-        const int H = live ? a.H : 0;
-        const int64_t tr = live ? t : 0;
-        const float rstd = live ? a.rstd[t] : 0.f;
+        const int H = t < a.T ? a.H : 0;
+        const int64_t tr = t < a.T ? t : 0;
+        const float rt = rstd;
         float g[VPT][8], xh[VPT][8];
         float along = 0.f;
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
             const int i = 8 * (int)(threadIdx.x + v * blockDim.x);
             float w[8];
-            load8<false>(static_cast<const __nv_bfloat16 *>(a.dout) + tr * a.ds, i, H, g[v]);
-            load8<R32>(static_cast<const char *>(a.h) + tr * a.hs * (R32 ? 4 : 2), i, H, xh[v]);
-            load8<W32>(a.w, i, H, w);
+            rg[v].floats(static_cast<const __nv_bfloat16 *>(a.dout) + tr * a.ds, i, H, g[v]);
+            rh[v].floats(static_cast<const char *>(a.h) + tr * a.hs * (R32 ? 4 : 2), i, H, xh[v]);
+            rw[v].floats(a.w, i, H, w);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                xh[v][j] *= rstd;
+                xh[v][j] *= rt;
                 dw[v][j] = fmaf(g[v][j], xh[v][j], dw[v][j]);
                 g[v][j] *= w[j];
                 along = fmaf(g[v][j], xh[v][j], along);
@@ -210,18 +249,21 @@ __global__ void __launch_bounds__(MAXT) add_rmsnorm_backward_kernel(NormBackArgs
         along = row_sum(along, red) / (float)a.H;
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
-            const int i = 8 * (int)(threadIdx.x + v * blockDim.x);
-            float d[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) d[j] = rstd * (g[v][j] - xh[v][j] * along);
+            for (int j = 0; j < 8; ++j) g[v][j] = rt * (g[v][j] - xh[v][j] * along);
             if (a.dsum) {
-                float s[8];
-                load8<R32>(static_cast<const char *>(a.dsum) + tr * a.ss * (R32 ? 4 : 2), i, H, s);
+                float d[8];
+                rs[v].floats(static_cast<const char *>(a.dsum) + tr * a.ss * (R32 ? 4 : 2),
+                             8 * (int)(threadIdx.x + v * blockDim.x), H, d);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) d[j] += s[j];
+                for (int j = 0; j < 8; ++j) g[v][j] += d[j];
             }
-            store8<R32>(static_cast<char *>(a.dx) + tr * a.os * (R32 ? 4 : 2), i, H, d);
         }
+        fetch((gr + gridDim.x) * blockDim.y + threadIdx.y);
+#pragma unroll
+        for (int v = 0; v < VPT; ++v)
+            store8<R32>(static_cast<char *>(a.dx) + tr * a.os * (R32 ? 4 : 2), 8 * (int)(threadIdx.x + v * blockDim.x),
+                        H, g[v]);
         __syncthreads();   // before the next rows write red
     }
     float *part = a.part + (int64_t)blockIdx.x * a.H;
@@ -275,6 +317,16 @@ NormShape norm_shape(int64_t chunks) {
     return n;
 }
 
+// The gradient holds more for each column (the column's sum, a second input): 2 chunks per
+// thread up to 8192 columns, 4 up to 16384, 8 above.
+NormShape norm_back_shape(int64_t chunks) {
+    NormShape n;
+    n.vpt = chunks <= 1024 ? 2 : chunks <= 2048 ? 4 : 8;
+    n.threads = (int)((chunks + 32 * n.vpt - 1) / (32 * n.vpt)) * 32;
+    n.rows = n.threads >= 256 ? 1 : 256 / n.threads;
+    return n;
+}
+
 int check_norm(const moe_norm *n) {
     if (!n) return MOE_ERR_INVALID_ARGUMENT;
     if (n->num_tokens < 0 || n->hidden < 1 || bad_dtype(n->residual_dtype) || bad_dtype(n->weight_dtype) ||
@@ -297,15 +349,16 @@ struct Shape {
     static constexpr int vpt = VPT, maxt = MAXT;
 };
 
-template <typename F>
+template <bool BACK, typename F>
 cudaError_t with_shape(const NormShape &sh, bool r32, bool w32, F &&f) {
     auto types = [&](auto v) {
         if (r32) return w32 ? f(v, std::true_type{}, std::true_type{}) : f(v, std::true_type{}, std::false_type{});
         return w32 ? f(v, std::false_type{}, std::true_type{}) : f(v, std::false_type{}, std::false_type{});
     };
-    if (sh.vpt == 2) return types(Shape<2, 256>{});
-    if (sh.vpt == 4) return types(Shape<4, 256>{});
-    if (sh.threads <= 256) return types(Shape<8, 256>{});
+    constexpr int wide = BACK ? 512 : 256;   // threads a row takes at most below the largest shape
+    if (sh.vpt == 2) return sh.threads <= 256 ? types(Shape<2, 256>{}) : types(Shape<2, wide>{});
+    if (sh.vpt == 4) return types(Shape<4, wide>{});
+    if (!BACK && sh.threads <= 256) return types(Shape<8, 256>{});
     return types(Shape<8, 1024>{});
 }
 
@@ -340,7 +393,7 @@ int moe_add_rmsnorm(const moe_norm *n, const void *x_dev, const void *residual_d
     a.shift_mask = even ? 0 : 15;
     const NormShape sh = norm_shape(((int64_t)n->hidden + (even ? 0 : 7) + 7) / 8);
     const dim3 grid((unsigned)(((int64_t)a.T + sh.rows - 1) / sh.rows)), block(sh.threads, sh.rows);
-    return status_of(with_shape(sh, n->residual_dtype == MOE_DTYPE_FP32, n->weight_dtype == MOE_DTYPE_FP32,
+    return status_of(with_shape<false>(sh, n->residual_dtype == MOE_DTYPE_FP32, n->weight_dtype == MOE_DTYPE_FP32,
                                 [&](auto v, auto r32, auto w32) {
                                     return launch_pdl(add_rmsnorm_kernel<decltype(v)::vpt, decltype(v)::maxt,
                                                                          decltype(r32)::value, decltype(w32)::value>,
@@ -373,7 +426,7 @@ int moe_add_rmsnorm_backward(const moe_norm *n, const void *dout_dev, const void
     if (workspace_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
     if ((rc = check_device()) != MOE_OK) return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const NormShape sh = norm_shape(((int64_t)n->hidden + 7) / 8);
+    const NormShape sh = norm_back_shape(((int64_t)n->hidden + 7) / 8);
     const int blocks = backward_blocks(n, sh);
     float *part = static_cast<float *>(workspace_dev);
     if (blocks > 0) {
@@ -381,7 +434,7 @@ int moe_add_rmsnorm_backward(const moe_norm *n, const void *dout_dev, const void
                        stride_of(n, n->residual_stride), stride_of(n, n->sum_stride),
                        stride_of(n, n->out_stride), n->num_tokens, n->hidden};
         const size_t smem = sh.rows > 1 ? (size_t)n->hidden * 4 : 0;   // at most 8 KB: rows > 1 below 2048 columns
-        const cudaError_t e = with_shape(
+        const cudaError_t e = with_shape<true>(
             sh, n->residual_dtype == MOE_DTYPE_FP32, n->weight_dtype == MOE_DTYPE_FP32,
             [&](auto v, auto r32, auto w32) {
                 return launch_pdl(add_rmsnorm_backward_kernel<decltype(v)::vpt, decltype(v)::maxt,
