@@ -5,13 +5,25 @@
 //     out[t] = sum_j w[t, j] * W2_e (silu(Wg_e x[t]) * (Wu_e x[t])),   W = (code - 8) * scale
 //
 // A decode batch has few rows for each expert, so the time is that of reading the picked
-// experts' codes once.  They feed warp-level matrix instructions (16 weight rows x 16 inputs
-// x 8 batch rows, bf16 with float32 sums): a tcgen05 tile of 128 rows would be nearly empty,
-// and its operands would have to be unpacked into shared memory first.  Codes become bf16
-// integers without rounding; the sums over a group of inputs are multiplied by its scale in
-// float32.  A block takes eight tiles of 16 weight rows; for 128 inputs at a time one warp
-// copies their codes and scales (contiguous in the prepared order) and the batch rows' inputs
-// to a ring of stages in shared memory, and four warps compute two tiles each.
+// experts' codes once, and what the kernels may spend on a code is little: at the HBM's rate
+// an SM has 22 cycles for the 1024 codes of 16 weight rows x 64 inputs, and its four
+// schedulers 88 instructions.  So
+//   - warp-level matrix instructions (16 weight rows x 16 inputs x 8 batch rows) take the
+//     codes almost as they are stored: the f16 numbers whose low bits are n and 16 n are
+//     n * 2^-24 and n * 2^-20, so a mask over a word of eight codes gives two matrix elements,
+//     and five instructions all eight.  (A tcgen05 tile's other side would be nearly empty,
+//     and its codes would have to pass through shared memory again.)
+//   - the 8 that a code is above its weight comes off through the sums of the inputs, where
+//     the matrix sum starts;
+//   - the inputs are f16 too: 64 of them at a time are divided by a power of two that brings
+//     the largest to 2^14 .. 2^15 (W4Inputs).  f16 holds the eight bits of x exactly; the
+//     activation is rounded to its eleven, four times finer than out's own rounding.
+// Products are exact, sums float32.  A block takes eight tiles of 16 weight rows; for 128
+// inputs at a time one warp copies their codes and scales (contiguous in the prepared order)
+// and the picks' inputs to a ring of stages in shared memory, and four warps compute two
+// tiles each.
+#include <cuda_fp16.h>
+
 #include "block_common.cuh"
 #include "tc_common.cuh"
 
@@ -22,24 +34,49 @@ constexpr int kW4Tiles = 8;    // tiles of 16 weight rows that a block takes at 
 constexpr int kW4Warps = 4;    // computing warps, two tiles each; one more warp copies
 constexpr int kW4Threads = (kW4Warps + 1) * 32;
 constexpr int kW4Blocks = 4;   // blocks on an SM
-constexpr int kW4Cols = 16;    // columns of inputs at a time
+constexpr int kW4Picks = 16;   // picks of one expert taken together
+constexpr int kW4FewPicks = 1024;   // up to which every block counts its pick's place itself
+
+// What goes with 64 f16 inputs of one row.  e: the power of two that they are to be multiplied
+// with; sum: theirs, of either 32, times -8 * 2^-24.
+struct __align__(16) W4Tail {
+    float e, sum[2], pad;
+};
+
+// 128 inputs of the row at `place` of the picks' order by expert, as a stage holds them.  The
+// inputs of eight rows from anywhere on lie on the banks that the eight lanes of a
+// shared-memory phase (two rows, four 16-byte pieces) want: 64 bytes past a multiple of 128
+// apart.  The tails of every other row take different slots.
+struct __align__(16) W4Inputs {
+    uint16_t v[128];
+    W4Tail tail[4];
+    static __host__ __device__ __forceinline__ int slot(int place, int half) { return ((place >> 1) + 2 * half) & 3; }
+};
+static_assert(sizeof(W4Inputs) == 320, "W4Inputs");
 
 struct W4Plan {
     int64_t T, H, E, k, I, P, G;
-    size_t head, rows, act, y, total;   // workspace offsets
+    size_t head, entries, picks, x, act, y, total;   // workspace offsets
 };
 
-// head: [0] number of picked experts, then their ids [E] and the starts of their rows [E + 1]
+// One run of up to kW4Picks picks of one expert.  An expert's runs follow each other; they work
+// through the same weights at the same time (W4Item).
+struct W4Entry {
+    int32_t expert, first, runs, begin, end, pad[3];   // the expert's first entry and their number; its places
+};
+
 struct W4Args {
     const uint16_t *x;
     const void *ids;
     const float *weights;
-    const uint4 *w1, *w2;
-    const uint16_t *s1, *s2;
-    uint16_t *out, *act;        // act [P][2][I]: bf16 pair (high, low) of the activation
+    const uint8_t *w1, *w2;
+    const uint8_t *s1, *s2;
+    uint16_t *out;
+    W4Inputs *xq, *act;         // [H / 128][P], [I / 128][P]: by place
     float *y;                   // [P][H]
-    int32_t *status, *head, *rows;
-    int T, H, E, k, I, P, ids64;
+    int32_t *status, *entries_used, *picks, *places;   // picks: by place; places: by pick
+    W4Entry *entries;
+    int T, H, E, k, I, P, ids64, placed;
 };
 
 __device__ __forceinline__ int load_id(const W4Args &a, int64_t p) {
@@ -47,13 +84,62 @@ __device__ __forceinline__ int load_id(const W4Args &a, int64_t p) {
     return v >= 0 && v < a.E ? (int)v : v == -1 ? -1 : -2;
 }
 
-// One block: the picks of each expert, the experts that have any.  The order of an expert's
-// rows is left open; every row's result is its own column of the products.
-__global__ void __launch_bounds__(1024) w4_group_kernel(W4Args a) {
+// 1 / e and e for the largest magnitude m of 64 inputs.
+__device__ __forceinline__ void power_scale(float m, float &down, float &e) {
+    const int b = min(max((int)(__float_as_uint(m) >> 23), 15), 254);   // m >= 0
+    down = __uint_as_float((uint32_t)(268 - b) << 23);
+    e = __uint_as_float((uint32_t)(b - 14) << 23);
+}
+
+// The place of pick p of expert e in the order by expert and pick: the valid picks before it.
+// All threads of the block call it.
+__device__ __forceinline__ int place_of(const W4Args &a, int p, int e) {
+    int before = 0;
+    for (int i = 0; i < a.P; i += 1024) {
+        const int o = i + (int)threadIdx.x < a.P ? load_id(a, i + threadIdx.x) : -1;
+        before += __syncthreads_count(o >= 0 && (o < e || (o == e && i + (int)threadIdx.x < p)));
+    }
+    return before;
+}
+
+// Block (1 + pick, 1024 inputs * 4) of x's f16 inputs: a warp to each 128, half a warp to each 64.
+__device__ __forceinline__ void w4_inputs_of_x(const W4Args &a, int p, int part) {
+    const int lane = threadIdx.x & 31, b = part * 32 + (threadIdx.x >> 5);
+    const int e = load_id(a, p);
+    if (e < 0) return;
+    const int place = a.placed ? a.places[p] : place_of(a, p, e);
+    if (b >= a.H / 128) return;
+    const uint2 in = reinterpret_cast<const uint2 *>(a.x + (int64_t)(p / a.k) * a.H + b * 128)[lane];
+    float m = fmaxf(fmaxf(fabsf(lo_f32(in.x)), fabsf(hi_f32(in.x))), fmaxf(fabsf(lo_f32(in.y)), fabsf(hi_f32(in.y))));
+#pragma unroll
+    for (int o = 8; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAllLanes, m, o));
+    float down, scale;
+    power_scale(m, down, scale);
+    const __half2 h0 = __floats2half2_rn(lo_f32(in.x) * down, hi_f32(in.x) * down);
+    const __half2 h1 = __floats2half2_rn(lo_f32(in.y) * down, hi_f32(in.y) * down);
+    float sum = (__low2float(h0) + __high2float(h0)) + (__low2float(h1) + __high2float(h1));
+#pragma unroll
+    for (int o = 4; o >= 1; o >>= 1) sum += __shfl_xor_sync(kAllLanes, sum, o);
+    W4Inputs &r = a.xq[(int64_t)b * a.P + place];
+    reinterpret_cast<__half2 *>(r.v)[2 * lane] = h0;
+    reinterpret_cast<__half2 *>(r.v)[2 * lane + 1] = h1;
+    W4Tail &tail = r.tail[W4Inputs::slot(place, lane / 16)];
+    if (lane % 8 == 0) tail.sum[lane / 8 % 2] = sum * -0x1p-21f;
+    if (lane % 16 == 0) tail.e = scale;
+}
+
+// Block 0 orders the picks by expert and lists the entries.  The others prepare x, counting
+// their pick's place themselves where there are few picks: one launch less; for many,
+// w4_inputs_kernel does it with the places that block 0 left (`placed`).
+__global__ void __launch_bounds__(1024) w4_group_kernel(W4Args a, int parts) {
     __shared__ int32_t count[MOE_MAX_EXPERTS], sums[64];
     __shared__ int32_t bad;
     pdl_begin();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (blockIdx.x > 0) {
+        w4_inputs_of_x(a, (blockIdx.x - 1) / parts, (blockIdx.x - 1) % parts);
+        return;
+    }
     for (int e = tid; e < MOE_MAX_EXPERTS; e += 1024) count[e] = 0;
     if (tid == 0) bad = 0;
     __syncthreads();
@@ -63,120 +149,107 @@ __global__ void __launch_bounds__(1024) w4_group_kernel(W4Args a) {
         if (e == -2) bad = 1;
     }
     __syncthreads();
-    // exclusive sums over the experts, two per thread: rows, and experts with rows
-    const int e0 = 2 * tid;
-    const int c0 = count[e0], c1 = count[e0 + 1];
-    int rows = c0 + c1, used = (c0 > 0) + (c1 > 0);
+    // exclusive sums over the experts, two per thread: picks, and entries
+    const int c[2] = {count[2 * tid], count[2 * tid + 1]};
+    const int n[2] = {(c[0] + kW4Picks - 1) / kW4Picks, (c[1] + kW4Picks - 1) / kW4Picks};
+    int picks = c[0] + c[1], runs = n[0] + n[1];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int r = __shfl_up_sync(kAllLanes, rows, o), u = __shfl_up_sync(kAllLanes, used, o);
+        const int r = __shfl_up_sync(kAllLanes, picks, o), u = __shfl_up_sync(kAllLanes, runs, o);
         if (lane >= o) {
-            rows += r;
-            used += u;
+            picks += r;
+            runs += u;
         }
     }
     if (lane == 31) {
-        sums[warp] = rows;
-        sums[32 + warp] = used;
+        sums[warp] = picks;
+        sums[32 + warp] = runs;
     }
     __syncthreads();
-    int rbase = 0, ubase = 0;
+    int r = picks - c[0] - c[1], u = runs - n[0] - n[1];
     for (int w = 0; w < warp; ++w) {
-        rbase += sums[w];
-        ubase += sums[32 + w];
+        r += sums[w];
+        u += sums[32 + w];
     }
-    int r = rbase + rows - c0 - c1, u = ubase + used - (c0 > 0) - (c1 > 0);
-    int32_t *ids = a.head + 1, *starts = a.head + 1 + a.E;
-    if (c0 > 0) {
-        ids[u] = e0;
-        starts[u++] = r;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        for (int i = 0; i < n[j]; ++i)
+            a.entries[u + i] = W4Entry{2 * tid + j, u, n[j], r + i * kW4Picks, r + min((i + 1) * kW4Picks, c[j]), {}};
+        count[2 * tid + j] = r;
+        r += c[j];
+        u += n[j];
     }
-    count[e0] = r;
-    r += c0;
-    if (c1 > 0) {
-        ids[u] = e0 + 1;
-        starts[u++] = r;
-    }
-    count[e0 + 1] = r;
-    r += c1;
     if (tid == 1023) {
-        a.head[0] = u;
-        starts[u] = r;
+        *a.entries_used = u;
         *a.status = bad ? MOE_STATUS_BAD_EXPERT_ID : 0;
     }
     __syncthreads();
-    for (int64_t p = tid; p < a.P; p += 1024) {
-        const int e = load_id(a, p);
-        if (e >= 0) a.rows[atomicAdd(&count[e], 1)] = (int)p;
+    // places in pick order: 32 picks at a time, warp after warp
+    for (int64_t p0 = 0; p0 < a.P; p0 += 1024) {
+        const int64_t p = p0 + tid;
+        const int e = p < a.P ? load_id(a, p) : -1;
+        const unsigned same = __match_any_sync(kAllLanes, e);
+        const int first = __ffs(same) - 1;
+        const int warps = (int)min((a.P - p0 + 31) / 32, (int64_t)32);
+        for (int w = 0; w < warps; ++w) {
+            if (warp == w) {
+                int base = 0;
+                if (e >= 0 && lane == first) {
+                    base = count[e];
+                    count[e] = base + __popc(same);
+                }
+                base = __shfl_sync(kAllLanes, base, first);
+                if (e >= 0) {
+                    const int place = base + __popc(same & ((1u << lane) - 1));
+                    a.picks[place] = (int)p;
+                    a.places[p] = place;
+                }
+            }
+            __syncthreads();
+        }
     }
 }
 
-// c (+)= a b; ZERO: the sum starts here.
-template <bool ZERO>
-__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    if (ZERO)
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
-            : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
-    else
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+__global__ void __launch_bounds__(1024) w4_inputs_kernel(W4Args a, int parts) {
+    pdl_begin();
+    w4_inputs_of_x(a, blockIdx.x / parts, blockIdx.x % parts);
 }
 
-// One matrix step of 16 inputs for NT blocks of columns: eight codes (nibble i + 4j: element j
-// of fragment register i) times b.  A code in the low mantissa bits of 128 is the bf16 number
-// 128 + code; 136 is taken off again, exactly.
-template <bool ZERO, int NT>
-__device__ __forceinline__ void w4_step(float (&part)[NT][4], uint32_t w, const uint32_t (&b0)[NT],
-                                        const uint32_t (&b1)[NT]) {
-    uint32_t f[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t v;   // (w >> 4i) & 0x000f000f | 0x43004300
-        asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(v) : "r"(w >> (4 * i)), "r"(0x000f000fu), "r"(0x43004300u));
-        const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&v), __float2bfloat162_rn(136.f));
-        f[i] = *reinterpret_cast<const uint32_t *>(&d);
-    }
-#pragma unroll
-    for (int n = 0; n < NT; ++n) mma_bf16<ZERO>(part[n], f, b0[n], b1[n]);
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0,
+                                        float c1, float c2, float c3) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
-// What a block works on at a time: kW4Tiles tiles of one expert for up to 16 columns of its
-// picks (PER columns a pick).  Walks the units (expert, tiles) of the call from block to block.
-template <int PER>
+// What a block works on at a time: kW4Tiles tiles of weight rows for one entry's picks.  The
+// units (entry, tiles) of the call go from block to block; an expert's entries take the same
+// tiles in neighbouring blocks, so that its weights come from memory once.
 struct W4Item {
-    int64_t u, group;
-    int i, begin, end;   // group of tiles within the expert; the picks a.rows[begin .. end) still to do
+    int64_t group;       // of tiles, in the matrix
+    int i, begin, n;     // of tiles, in the expert; the picks a.picks[begin .. begin + n)
 
-    __device__ __forceinline__ int picks() const { return min(end - begin, kW4Cols / PER); }
-    __device__ __forceinline__ bool start(const W4Args &a, int groups, int64_t units) {
+    __device__ __forceinline__ bool load(const W4Args &a, int64_t u, int groups, int64_t units) {
         if (u >= units) return false;
-        const int which = (int)(u / groups);
-        const int32_t *ids = a.head + 1, *starts = a.head + 1 + a.E;
-        i = (int)(u - (int64_t)which * groups);
-        group = (int64_t)ids[which] * groups + i;
-        begin = starts[which];
-        end = starts[which + 1];
+        const W4Entry first = a.entries[u / groups];
+        const int64_t local = u - (int64_t)first.first * groups;   // in the expert's entries
+        i = (int)(local / first.runs);
+        const W4Entry e = a.entries[first.first + (int)(local - (int64_t)i * first.runs)];
+        group = (int64_t)e.expert * groups + i;
+        begin = e.begin;
+        n = e.end - e.begin;
         return true;
-    }
-    __device__ __forceinline__ bool advance(const W4Args &a, int groups, int64_t units) {
-        begin += picks();
-        if (begin < end) return true;
-        u += gridDim.x;
-        return start(a, groups, units);
     }
 };
 
-// A stage holds 128 inputs: the tiles' codes and scales, and the columns' inputs.  The columns
-// lie 64 bytes more apart than they are long, so that the eight lanes of a shared-memory phase
-// (two columns, four 16-byte pieces) fall on different banks.
+// A stage holds 128 inputs: the tiles' codes and scales, and the rows.
 template <int G>
 struct W4Stage {
     static constexpr int kPairs = 128 / G;   // scale pairs (rows g, g + 8) per 128 inputs
-    static constexpr int kCodes = kW4Tiles * 1024, kScales = kW4Tiles * 32 * kPairs, kColumn = 256 + 64;
-    static constexpr int kBytes = kCodes + kScales + kW4Cols * kColumn;
-    static constexpr int kStages = G == 32 ? 3 : 4;   // what fits four blocks of an SM
+    static constexpr int kCodes = kW4Tiles * 1024, kScales = kW4Tiles * 32 * kPairs;
+    static constexpr int kBytes = kCodes + kScales + kW4Picks * (int)sizeof(W4Inputs);
+    static constexpr int kStages = (227 * 1024 / kW4Blocks - 3072) / kBytes;
+    static_assert(kStages >= 3, "stages");
 };
 
 __device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
@@ -185,39 +258,64 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_
                  : "memory");
 }
 
-// One stage for the warp's two tiles: acc[t][n][.] += tile t times column block n.
-template <int NT, int G>
-__device__ __forceinline__ void w4_compute(const uint8_t *stage, int warp, float (&acc)[2][NT][4]) {
+// One stage for the warp's two tiles: acc[t][r] += tile t times picks 8r .. 8r + 7.  tails[j]:
+// where in the stage the first 64 inputs' tail of pick 2q + j is (of pick 8 + 2q + j: the same
+// slot eight rows on; of the second 64 inputs: two slots on).
+template <int G, int RB>
+__device__ __forceinline__ void w4_compute(const uint8_t *stage, int warp, const int (&tails)[2], float (&acc)[2][RB][4]) {
     using S = W4Stage<G>;
     constexpr int kPairs = S::kPairs;
     const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
     const uint4 *w = reinterpret_cast<const uint4 *>(stage) + warp * 2 * 64 + lane;
     const uint32_t *sc = reinterpret_cast<const uint32_t *>(stage + S::kCodes) + (warp * 2 * 8 + g) * kPairs;
-    const uint8_t *x = stage + S::kCodes + S::kScales + g * S::kColumn + q * 16;
-    float part[2][NT][4];
-    uint4 v[2];
+    const W4Inputs *in = reinterpret_cast<const W4Inputs *>(stage + S::kCodes + S::kScales);
 #pragma unroll
-    for (int h = 0; h < 4; ++h) {   // 32 inputs: two matrix steps
-        uint32_t b0[NT], b1[NT], b2[NT], b3[NT];
+    for (int c = 0; c < 2; ++c) {   // 64 inputs
+        asm volatile("" ::: "memory");   // their loads stay here: registers
+        uint4 b[RB][2];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const uint4 b = *reinterpret_cast<const uint4 *>(x + n * 8 * S::kColumn + h * 64);
-            b0[n] = b.x; b1[n] = b.y; b2[n] = b.z; b3[n] = b.w;
-        }
+        for (int r = 0; r < RB; ++r)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) b[r][h] = reinterpret_cast<const uint4 *>(in[8 * r + g].v)[c * 8 + h * 4 + q];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            if (h % 2 == 0) v[t] = w[t * 64 + h / 2 * 32];
-            if (h * 32 % G == 0) w4_step<true, NT>(part[t], h % 2 ? v[t].z : v[t].x, b0, b1);
-            else w4_step<false, NT>(part[t], h % 2 ? v[t].z : v[t].x, b0, b1);
-            w4_step<false, NT>(part[t], h % 2 ? v[t].w : v[t].y, b2, b3);
-            if ((h + 1) * 32 % G == 0) {
-                const uint32_t p = sc[t * 8 * kPairs + h * 32 / G];
+            if (RB > 1) asm volatile("" ::: "memory");
+            const uint4 v = w[t * 64 + c * 32];
+            const uint8_t *tail[2];   // of this lane's columns of sums
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    acc[t][n][0] = fmaf(lo_f32(p), part[t][n][0], acc[t][n][0]);
-                    acc[t][n][1] = fmaf(lo_f32(p), part[t][n][1], acc[t][n][1]);
-                    acc[t][n][2] = fmaf(hi_f32(p), part[t][n][2], acc[t][n][2]);
-                    acc[t][n][3] = fmaf(hi_f32(p), part[t][n][3], acc[t][n][3]);
+            for (int j = 0; j < 2; ++j) tail[j] = stage + (tails[j] ^ (c * 2 * (int)sizeof(W4Tail)));
+            float part[RB][4];
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {   // 16 inputs, a matrix step
+                const uint32_t w0 = s == 0 ? v.x : s == 1 ? v.y : s == 2 ? v.z : v.w, w1 = w0 >> 8;
+                const uint32_t f[4] = {w0 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x000f000fu, w1 & 0x00f000f0u};
+#pragma unroll
+                for (int r = 0; r < RB; ++r) {
+                    const uint4 &bb = b[r][s / 2];
+                    const uint32_t b0 = s % 2 ? bb.z : bb.x, b1 = s % 2 ? bb.w : bb.y;
+                    if (s == 0 || (s == 2 && G == 32)) {   // the sum starts at -8 times the inputs' sum
+                        float z[2];
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const W4Tail *p = reinterpret_cast<const W4Tail *>(tail[j] + r * 8 * sizeof(W4Inputs));
+                            z[j] = G == 32 ? p->sum[s / 2] : p->sum[0] + p->sum[1];
+                        }
+                        mma_f16(part[r], f, b0, b1, z[0], z[1], 16.f * z[0], 16.f * z[1]);
+                    } else {
+                        mma_f16(part[r], f, b0, b1, part[r][0], part[r][1], part[r][2], part[r][3]);
+                    }
+                }
+                if (s == 3 || (s == 1 && G == 32)) {   // the end of a scale's group or of the 64 inputs
+                    const uint32_t sp = sc[t * 8 * kPairs + (c * 64 + s * 16) / G];
+#pragma unroll
+                    for (int r = 0; r < RB; ++r) {
+                        const float e0 = reinterpret_cast<const W4Tail *>(tail[0] + r * 8 * sizeof(W4Inputs))->e;
+                        const float e1 = reinterpret_cast<const W4Tail *>(tail[1] + r * 8 * sizeof(W4Inputs))->e;
+                        acc[t][r][0] = fmaf(lo_f32(sp) * e0, part[r][0], acc[t][r][0]);
+                        acc[t][r][1] = fmaf(lo_f32(sp) * e1, part[r][1], acc[t][r][1]);
+                        acc[t][r][2] = fmaf(hi_f32(sp) * e0, part[r][2], acc[t][r][2]);
+                        acc[t][r][3] = fmaf(hi_f32(sp) * e1, part[r][3], acc[t][r][3]);
+                    }
                 }
             }
         }
@@ -226,43 +324,7 @@ __device__ __forceinline__ void w4_compute(const uint8_t *stage, int warp, float
 
 __device__ __forceinline__ float silu(float v) { return __fdiv_rn(v, 1.0f + expf(-v)); }
 
-// First product: a tile is rows i0 .. i0 + 7 of the gate and of the up matrix (its rows 0..7
-// and 8..15), so a lane holds both factors of its activations.
-template <int NT>
-__device__ __forceinline__ void w4_store_act(const W4Args &a, int i0, const int32_t *rows, int n,
-                                             const float (&acc)[NT][4]) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-#pragma unroll
-    for (int b = 0; b < NT; ++b)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int c = 8 * b + 2 * q + j;
-            if (c >= n) continue;
-            const float h = silu(acc[b][j]) * acc[b][2 + j];
-            const __nv_bfloat16 hi = __float2bfloat16_rn(h);
-            const float back = __bfloat162float(hi);
-            const __nv_bfloat16 lo = __float2bfloat16_rn(isinf(back) ? 0.f : h - back);
-            uint16_t *o = a.act + (int64_t)rows[c] * 2 * a.I + i0 + g;
-            o[0] = __bfloat16_as_ushort(hi);
-            o[a.I] = __bfloat16_as_ushort(lo);
-        }
-}
-
-// Second product: columns 2r and 2r + 1 are the high and the low part of pick r's activation,
-// whose products are added here.
-template <int NT>
-__device__ __forceinline__ void w4_store_y(const W4Args &a, int h0, const int32_t *rows, int n,
-                                           const float (&acc)[NT][4]) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-#pragma unroll
-    for (int b = 0; b < NT; ++b) {
-        const int r = 4 * b + q;
-        if (r >= n) continue;
-        float *o = a.y + (int64_t)rows[r] * a.H + h0 + g;
-        o[0] = acc[b][0] + acc[b][1];
-        o[8] = acc[b][2] + acc[b][3];
-    }
-}
+__device__ __forceinline__ void computing_warps_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kW4Warps * 32) : "memory"); }
 
 // UP: the first product and the activation; else the second product.
 template <bool UP, int G>
@@ -270,6 +332,8 @@ __global__ void __launch_bounds__(kW4Threads, kW4Blocks) w4_product_kernel(W4Arg
     using S = W4Stage<G>;
     extern __shared__ __align__(128) uint8_t stages[];   // [kStages][kBytes]
     __shared__ __align__(8) uint64_t full[S::kStages], empty[S::kStages];
+    __shared__ __align__(16) uint16_t acts[8][64];
+    __shared__ float top[kW4Warps][8], sums[kW4Warps][8], scale[8];
     __shared__ int abort_flag;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
@@ -282,13 +346,9 @@ __global__ void __launch_bounds__(kW4Threads, kW4Blocks) w4_product_kernel(W4Arg
     }
     __syncthreads();
     pdl_begin();
-    const int K = UP ? a.H : a.I, blocks = K / 128;
+    const int blocks = (UP ? a.H : a.I) / 128;   // stages of an item
     const int groups = (UP ? a.I / 8 : a.H / 16) / kW4Tiles;
-    const int64_t units = (int64_t)a.head[0] * groups;
-    constexpr int kPer = UP ? 1 : 2;
-    W4Item<kPer> it;
-    it.u = blockIdx.x;
-    if (!it.start(a, groups, units)) return;
+    const int64_t units = (int64_t)*a.entries_used * groups;
     int stage = 0;
     uint32_t phase = 0;
     auto next_stage = [&] {
@@ -297,40 +357,43 @@ __global__ void __launch_bounds__(kW4Threads, kW4Blocks) w4_product_kernel(W4Arg
             phase ^= 1;
         }
     };
+    W4Item it;
 
-    if (warp == kW4Warps) {   // the copying warp: lanes 0..15 a column each, 16 codes, 17 scales
+    if (warp == kW4Warps) {   // the copying warp: lane 0 the codes, 1 the scales, 2 the rows
         int put = 0;
         bool ok = true;
-        do {
-            const int n = it.picks() * kPer;
-            const char *src = nullptr;
-            uint32_t bytes = 0, off = 0;
-            int step = 0;
-            if (lane < n) {
-                const int64_t p = a.rows[it.begin + lane / kPer];
-                src = reinterpret_cast<const char *>(UP ? a.x + p / a.k * a.H : a.act + (p * 2 + (lane & 1)) * a.I);
-                bytes = step = 256;
-                off = S::kCodes + S::kScales + lane * S::kColumn;
-            } else if (lane == 16) {
-                src = reinterpret_cast<const char *>(UP ? a.w1 : a.w2) + it.group * blocks * S::kCodes;
+        for (int64_t u = blockIdx.x; ok && it.load(a, u, groups, units); u += gridDim.x) {
+            const uint8_t *src;
+            uint32_t bytes, off;
+            int64_t step;
+            if (lane == 0) {
+                src = (UP ? a.w1 : a.w2) + it.group * blocks * S::kCodes;
                 bytes = step = S::kCodes;
-            } else if (lane == 17) {
-                src = reinterpret_cast<const char *>(UP ? a.s1 : a.s2) + it.group * blocks * S::kScales;
+                off = 0;
+            } else if (lane == 1) {
+                src = (UP ? a.s1 : a.s2) + it.group * blocks * S::kScales;
                 bytes = step = S::kScales;
                 off = S::kCodes;
+            } else {
+                src = reinterpret_cast<const uint8_t *>((UP ? a.xq : a.act) + it.begin);
+                bytes = it.n * (uint32_t)sizeof(W4Inputs);
+                step = (int64_t)a.P * sizeof(W4Inputs);
+                off = S::kCodes + S::kScales;
             }
             for (int b = 0; b < blocks; ++b) {
                 ok = mbar_wait(smem_u32(empty + stage), phase ^ 1, &abort_flag, a.status);
                 ok = __all_sync(kAllLanes, ok);
                 if (!ok) break;
-                if (lane == 0) mbar_expect_tx(smem_u32(full + stage), S::kCodes + S::kScales + n * 256);
+                const uint32_t bar = smem_u32(full + stage);
+                if (lane == 0)
+                    mbar_expect_tx(bar, S::kCodes + S::kScales + it.n * (uint32_t)sizeof(W4Inputs));
                 __syncwarp();
-                if (bytes) bulk_copy(smem_u32(stages) + stage * S::kBytes + off, src, bytes, smem_u32(full + stage));
+                if (lane < 3) bulk_copy(smem_u32(stages) + stage * S::kBytes + off, src, bytes, bar);
                 src += step;
                 ++put;
                 next_stage();
             }
-        } while (ok && it.advance(a, groups, units));
+        }
         if (!ok) {
             // gave up: the copies under way may not outlive the block, so each stage's gets one
             // more bounded wait (the status word already holds MOE_STATUS_TIMEOUT)
@@ -343,30 +406,89 @@ __global__ void __launch_bounds__(kW4Threads, kW4Blocks) w4_product_kernel(W4Arg
         return;
     }
 
-    do {
-        const int32_t *rows = a.rows + it.begin;
-        const int n = it.picks();
-        const int first = (it.i * kW4Tiles + warp * 2) * (UP ? 8 : 16);   // of the warp's first tile
-        auto run = [&](auto blocks_of_columns) {
-            constexpr int NT = decltype(blocks_of_columns)::value;
-            float acc[2][NT][4] = {};
-            for (int b = 0; b < blocks; ++b) {
-                const bool in = mbar_wait(smem_u32(full + stage), phase, &abort_flag, a.status);
-                if (!__all_sync(kAllLanes, in)) return false;
-                w4_compute<NT, G>(stages + stage * S::kBytes, warp, acc);
-                __syncwarp();   // every lane has read the stage
-                if (lane == 0) mbar_arrive(smem_u32(empty + stage));
-                next_stage();
-            }
+    // A warp whose wait ran out (the status word then holds MOE_STATUS_TIMEOUT) goes on through
+    // the units without waiting or computing: the others may stand at the warps' barrier.
+    const int g = lane >> 2, q = lane & 3;
+    bool ok = true;
+    auto unit = [&](auto blocks_of_picks) {
+        constexpr int RB = decltype(blocks_of_picks)::value;
+        float acc[2][RB][4] = {};
+        int tails[2];
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                if constexpr (UP) w4_store_act<NT>(a, first + 8 * t, rows, n, acc[t]);
-                else w4_store_y<NT>(a, first + 16 * t, rows, n, acc[t]);
+        for (int j = 0; j < 2; ++j)
+            tails[j] = S::kCodes + S::kScales + (2 * q + j) * (int)sizeof(W4Inputs) + (int)offsetof(W4Inputs, tail) +
+                       W4Inputs::slot(it.begin + 2 * q + j, 0) * (int)sizeof(W4Tail);
+        for (int b = 0; b < blocks && ok; ++b) {
+            ok = mbar_wait(smem_u32(full + stage), phase, &abort_flag, a.status);
+            ok = __all_sync(kAllLanes, ok);
+            if (!ok) break;
+            w4_compute<G, RB>(stages + stage * S::kBytes, warp, tails, acc);
+            __syncwarp();   // every lane has read the stage
+            if (lane == 0) mbar_arrive(smem_u32(empty + stage));
+            next_stage();
+        }
+#pragma unroll
+        for (int r = 0; r < RB; ++r) {
+            // the codes' 2^-24 (rows 0..7 of a tile) and 2^-20 (rows 8..15)
+            if constexpr (UP) {
+                // Rows 0..7 of a tile are gate rows, 8..15 the same up rows: a lane has both
+                // factors of inputs 16 warp + 8t + g of the unit's 64, of picks 2q and 2q + 1.
+                float h[2][2];   // [tile][pick]
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) h[t][j] = silu(acc[t][r][j] * 0x1p24f) * (acc[t][r][2 + j] * 0x1p20f);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    float m = fmaxf(fabsf(h[0][j]), fabsf(h[1][j]));
+#pragma unroll
+                    for (int o = 4; o <= 16; o <<= 1) m = fmaxf(m, __shfl_xor_sync(kAllLanes, m, o));
+                    if (g == 0) top[warp][2 * q + j] = m;
+                }
+                computing_warps_sync();
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int c = 2 * q + j;
+                    float down, e;
+                    power_scale(fmaxf(fmaxf(top[0][c], top[1][c]), fmaxf(top[2][c], top[3][c])), down, e);
+                    const __half2 v = __floats2half2_rn(h[0][j] * down, h[1][j] * down);
+                    acts[c][16 * warp + g] = __half_as_ushort(__low2half(v));
+                    acts[c][16 * warp + 8 + g] = __half_as_ushort(__high2half(v));
+                    float sum = __low2float(v) + __high2float(v);
+#pragma unroll
+                    for (int o = 4; o <= 16; o <<= 1) sum += __shfl_xor_sync(kAllLanes, sum, o);
+                    if (g == 0) sums[warp][c] = sum;
+                    if (g == 0 && warp == 0) scale[c] = e;
+                }
+                computing_warps_sync();
+                const int c = threadIdx.x >> 3, v = threadIdx.x & 7;   // pick, 8 of its 64 inputs
+                if (c < min(8, it.n - 8 * r)) {
+                    const int place = it.begin + 8 * r + c;
+                    W4Inputs &o = a.act[(int64_t)(it.i >> 1) * a.P + place];
+                    reinterpret_cast<uint4 *>(o.v)[(it.i & 1) * 8 + v] = reinterpret_cast<const uint4 *>(acts[c])[v];
+                    if (v == 0)
+                        *reinterpret_cast<float4 *>(&o.tail[W4Inputs::slot(place, it.i & 1)]) =
+                            make_float4(scale[c], (sums[0][c] + sums[1][c]) * -0x1p-21f, (sums[2][c] + sums[3][c]) * -0x1p-21f, 0.f);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int c = 8 * r + 2 * q + j;
+                    if (c >= it.n) continue;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        float *o = a.y + (int64_t)a.picks[it.begin + c] * a.H + (it.i * kW4Tiles + warp * 2 + t) * 16 + g;
+                        o[0] = acc[t][r][j] * 0x1p24f;
+                        o[8] = acc[t][r][2 + j] * 0x1p20f;
+                    }
+                }
             }
-            return true;
-        };
-        if (!(n * kPer <= 8 ? run(std::integral_constant<int, 1>{}) : run(std::integral_constant<int, 2>{}))) return;
-    } while (it.advance(a, groups, units));
+        }
+    };
+    for (int64_t u = blockIdx.x; it.load(a, u, groups, units); u += gridDim.x) {
+        if (it.n <= 8) unit(std::integral_constant<int, 1>{});
+        else unit(std::integral_constant<int, 2>{});
+    }
 }
 
 // out[t] = sum over the picks, in their order, of weight * y; eight columns per thread.
@@ -392,11 +514,10 @@ __global__ void __launch_bounds__(256) w4_combine_kernel(W4Args a) {
 
 // Prepared order.  A tile is 16 weight rows: half = rows / 2 > 0 pairs rows i0 .. i0 + 7 with
 // rows half + i0 .. (gate and up of w1), half == 0 takes 16 consecutive rows.  For 64 inputs
-// from k0 on, lane (g, q) of a tile holds rows g and g + 8, inputs k0 + 8q .. + 7 and
-// k0 + 32 + 8q .. + 7: word s (matrix step s) has nibble i + 4j = element j of fragment
-// register i, where registers 0, 2 are row g and 1, 3 row g + 8, and registers 2, 3 the next
-// two inputs.  The order is [8 tiles][128 inputs][tile][64 inputs][lane]; one thread per lane
-// and 64 inputs.
+// from k0 on, lane (g, q) of a tile holds rows g and g + 8 of inputs k0 + 32h + 8q .. + 7, h =
+// 0, 1: word 2h + s has inputs 4s .. 4s + 3 of these in its bytes 0, 2, 1, 3, row g's code in a
+// byte's low half and row g + 8's in its high one.  The order is [8 tiles][128 inputs][tile][64 inputs][lane];
+// one thread per lane and 64 inputs.
 __global__ void __launch_bounds__(256) w4_order_codes_kernel(const uint8_t *codes, uint4 *out, int64_t n, int rows,
                                                              int K, int half) {
     const int64_t v = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -475,9 +596,11 @@ int make_w4_plan(const moe_w4_geom *g, W4Plan *p) {
         off = (off + bytes + 255) / 256 * 256;
         return o;
     };
-    p->head = take(4 * (2 * p->E + 2));
-    p->rows = take(4 * p->P);
-    p->act = take(4 * p->P * p->I);
+    p->head = take(4);
+    p->entries = take(sizeof(W4Entry) * (p->P < p->E ? p->P : p->E) + sizeof(W4Entry) * (p->P / kW4Picks));
+    p->picks = take(8 * p->P);
+    p->x = take(sizeof(W4Inputs) * p->P * (p->H / 128));
+    p->act = take(sizeof(W4Inputs) * p->P * (p->I / 128));
     p->y = take(4 * p->P * p->H);
     p->total = off;
     return MOE_OK;
@@ -499,7 +622,7 @@ cudaError_t order_matrix(const uint8_t *codes, const void *scales, uint8_t *out,
 }
 
 template <bool UP, int G>
-cudaError_t launch_product_of(const W4Args &a, unsigned blocks, cudaStream_t s) {
+cudaError_t launch_product_of(const W4Args &a, int64_t units, cudaStream_t s) {
     constexpr int smem = W4Stage<G>::kStages * W4Stage<G>::kBytes;
     static std::once_flag once[64];   // per device
     static cudaError_t set[64];
@@ -509,16 +632,16 @@ cudaError_t launch_product_of(const W4Args &a, unsigned blocks, cudaStream_t s) 
         set[dev] = cudaFuncSetAttribute(w4_product_kernel<UP, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     });
     if (set[dev] != cudaSuccess) return set[dev];
-    return launch_pdl(w4_product_kernel<UP, G>, dim3(blocks), dim3(kW4Threads), smem, s, a);
+    const int64_t most = kW4Blocks * (int64_t)num_sms();
+    return launch_pdl(w4_product_kernel<UP, G>, dim3((unsigned)(units < most ? units : most)), dim3(kW4Threads), smem,
+                      s, a);
 }
 
 template <bool UP>
-cudaError_t launch_product(const W4Args &a, int64_t G, int64_t most_units, cudaStream_t s) {
-    const int64_t most = kW4Blocks * (int64_t)num_sms();
-    const unsigned blocks = (unsigned)(most_units < most ? most_units : most);
-    if (G == 32) return launch_product_of<UP, 32>(a, blocks, s);
-    if (G == 64) return launch_product_of<UP, 64>(a, blocks, s);
-    return launch_product_of<UP, 128>(a, blocks, s);
+cudaError_t launch_product(const W4Args &a, int64_t G, int64_t units, cudaStream_t s) {
+    if (G == 32) return launch_product_of<UP, 32>(a, units, s);
+    if (G == 64) return launch_product_of<UP, 64>(a, units, s);
+    return launch_product_of<UP, 128>(a, units, s);
 }
 
 }  // namespace
@@ -601,18 +724,35 @@ int moe_forward_w4(const moe_w4_geom *g, const void *x_dev, const void *topk_ids
     if ((rc = check_device()) != MOE_OK) return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     char *ws = static_cast<char *>(workspace_dev);
-    W4Args a{static_cast<const uint16_t *>(x_dev), topk_ids_dev, topk_weights_dev,
-             reinterpret_cast<const uint4 *>(w1_prepared_dev), reinterpret_cast<const uint4 *>(w2_prepared_dev),
-             static_cast<const uint16_t *>(w1_scales_prepared_dev),
-             static_cast<const uint16_t *>(w2_scales_prepared_dev), static_cast<uint16_t *>(out_dev),
-             reinterpret_cast<uint16_t *>(ws + p.act), reinterpret_cast<float *>(ws + p.y), status_dev,
-             reinterpret_cast<int32_t *>(ws + p.head), reinterpret_cast<int32_t *>(ws + p.rows), (int)p.T, (int)p.H,
-             (int)p.E, (int)p.k, (int)p.I, (int)p.P, ids_dtype == MOE_IDS_INT64};
-    cudaError_t e = launch_pdl(w4_group_kernel, dim3(1), dim3(1024), 0, s, a);
+    W4Args a{};
+    a.x = static_cast<const uint16_t *>(x_dev);
+    a.ids = topk_ids_dev;
+    a.weights = topk_weights_dev;
+    a.w1 = w1_prepared_dev;
+    a.w2 = w2_prepared_dev;
+    a.s1 = static_cast<const uint8_t *>(w1_scales_prepared_dev);
+    a.s2 = static_cast<const uint8_t *>(w2_scales_prepared_dev);
+    a.out = static_cast<uint16_t *>(out_dev);
+    a.xq = reinterpret_cast<W4Inputs *>(ws + p.x);
+    a.act = reinterpret_cast<W4Inputs *>(ws + p.act);
+    a.y = reinterpret_cast<float *>(ws + p.y);
+    a.status = status_dev;
+    a.entries_used = reinterpret_cast<int32_t *>(ws + p.head);
+    a.picks = reinterpret_cast<int32_t *>(ws + p.picks);
+    a.places = a.picks + p.P;
+    a.entries = reinterpret_cast<W4Entry *>(ws + p.entries);
+    a.T = (int)p.T; a.H = (int)p.H; a.E = (int)p.E; a.k = (int)p.k; a.I = (int)p.I; a.P = (int)p.P;
+    a.ids64 = ids_dtype == MOE_IDS_INT64;
+    const int parts = (int)((p.H / 128 + 31) / 32);   // blocks that prepare one pick's x
+    if (p.P * parts + 1 >= ((int64_t)1 << 31)) return MOE_ERR_LIMIT;
+    a.placed = p.P > kW4FewPicks;
+    cudaError_t e = launch_pdl(w4_group_kernel, dim3((unsigned)(1 + (a.placed ? 0 : p.P * parts))), dim3(1024), 0, s, a, parts);
+    if (e == cudaSuccess && a.placed)
+        e = launch_pdl(w4_inputs_kernel, dim3((unsigned)(p.P * parts)), dim3(1024), 0, s, a, parts);
     if (e == cudaSuccess && p.T > 0) {
-        const int64_t used = p.P < p.E ? p.P : p.E;   // experts that can have picks
-        e = launch_product<true>(a, p.G, used * (p.I / 8 / kW4Tiles), s);
-        if (e == cudaSuccess) e = launch_product<false>(a, p.G, used * (p.H / 16 / kW4Tiles), s);
+        const int64_t entries = (p.P < p.E ? p.P : p.E) + p.P / kW4Picks;   // at most
+        e = launch_product<true>(a, p.G, entries * (p.I / 8 / kW4Tiles), s);
+        if (e == cudaSuccess) e = launch_product<false>(a, p.G, entries * (p.H / 16 / kW4Tiles), s);
         if (e == cudaSuccess)
             e = launch_pdl(w4_combine_kernel, dim3(blocks256(p.T * (p.H / 8))), dim3(256), 0, s, a);
     }
