@@ -20,8 +20,9 @@
 //     activation is rounded to its eleven, four times finer than out's own rounding.
 // Products are exact, sums float32.  A block takes eight tiles of 16 weight rows; for 128
 // inputs at a time one warp copies their codes and scales (contiguous in the prepared order)
-// and the picks' inputs to a ring of stages in shared memory, and four warps compute two
-// tiles each.
+// and the picks' inputs to a ring of stages in shared memory, and eight warps compute: two
+// groups of four, two tiles a warp, take turns at the stages and add up at the end.  (A unit
+// then has two warps on each scheduler even where there are fewer units than room for them.)
 #include <cuda_fp16.h>
 
 #include "block_common.cuh"
@@ -31,10 +32,10 @@ namespace moe {
 namespace {
 
 constexpr int kW4Tiles = 8;    // tiles of 16 weight rows that a block takes at a time
-constexpr int kW4Warps = 4;    // computing warps, two tiles each; one more warp copies
-constexpr int kW4Threads = (kW4Warps + 1) * 32;
-constexpr int kW4Blocks = 4;   // blocks on an SM
-constexpr int kW4Picks = 16;   // picks of one expert taken together
+constexpr int kW4Warps = 4;    // computing warps of a group, two tiles each
+constexpr int kW4Threads = (2 * kW4Warps + 1) * 32;   // two groups, and one more warp that copies
+constexpr int kW4Blocks = 2;   // blocks on an SM
+constexpr int kW4Picks = 8;    // picks of one expert taken together
 constexpr int kW4FewPicks = 1024;   // up to which every block counts its pick's place itself
 
 // What goes with 64 f16 inputs of one row.  e: the power of two that they are to be multiplied
@@ -102,42 +103,43 @@ __device__ __forceinline__ int place_of(const W4Args &a, int p, int e) {
     return before;
 }
 
-// Block (1 + pick, 1024 inputs * 4) of x's f16 inputs: a warp to each 128, half a warp to each 64.
-__device__ __forceinline__ void w4_inputs_of_x(const W4Args &a, int p, int part) {
-    const int lane = threadIdx.x & 31, b = part * 32 + (threadIdx.x >> 5);
+// The f16 inputs of pick p: a warp to each 128 of them, half a warp to each 64.
+__device__ __forceinline__ void w4_inputs_of_x(const W4Args &a, int p) {
+    const int lane = threadIdx.x & 31;
     const int e = load_id(a, p);
     if (e < 0) return;
     const int place = a.placed ? a.places[p] : place_of(a, p, e);
-    if (b >= a.H / 128) return;
-    const uint2 in = reinterpret_cast<const uint2 *>(a.x + (int64_t)(p / a.k) * a.H + b * 128)[lane];
-    float m = fmaxf(fmaxf(fabsf(lo_f32(in.x)), fabsf(hi_f32(in.x))), fmaxf(fabsf(lo_f32(in.y)), fabsf(hi_f32(in.y))));
+    for (int b = threadIdx.x >> 5; b < a.H / 128; b += 32) {
+        const uint2 in = reinterpret_cast<const uint2 *>(a.x + (int64_t)(p / a.k) * a.H + b * 128)[lane];
+        float m = fmaxf(fmaxf(fabsf(lo_f32(in.x)), fabsf(hi_f32(in.x))), fmaxf(fabsf(lo_f32(in.y)), fabsf(hi_f32(in.y))));
 #pragma unroll
-    for (int o = 8; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAllLanes, m, o));
-    float down, scale;
-    power_scale(m, down, scale);
-    const __half2 h0 = __floats2half2_rn(lo_f32(in.x) * down, hi_f32(in.x) * down);
-    const __half2 h1 = __floats2half2_rn(lo_f32(in.y) * down, hi_f32(in.y) * down);
-    float sum = (__low2float(h0) + __high2float(h0)) + (__low2float(h1) + __high2float(h1));
+        for (int o = 8; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAllLanes, m, o));
+        float down, scale;
+        power_scale(m, down, scale);
+        const __half2 h0 = __floats2half2_rn(lo_f32(in.x) * down, hi_f32(in.x) * down);
+        const __half2 h1 = __floats2half2_rn(lo_f32(in.y) * down, hi_f32(in.y) * down);
+        float sum = (__low2float(h0) + __high2float(h0)) + (__low2float(h1) + __high2float(h1));
 #pragma unroll
-    for (int o = 4; o >= 1; o >>= 1) sum += __shfl_xor_sync(kAllLanes, sum, o);
-    W4Inputs &r = a.xq[(int64_t)b * a.P + place];
-    reinterpret_cast<__half2 *>(r.v)[2 * lane] = h0;
-    reinterpret_cast<__half2 *>(r.v)[2 * lane + 1] = h1;
-    W4Tail &tail = r.tail[W4Inputs::slot(place, lane / 16)];
-    if (lane % 8 == 0) tail.sum[lane / 8 % 2] = sum * -0x1p-21f;
-    if (lane % 16 == 0) tail.e = scale;
+        for (int o = 4; o >= 1; o >>= 1) sum += __shfl_xor_sync(kAllLanes, sum, o);
+        W4Inputs &r = a.xq[(int64_t)b * a.P + place];
+        reinterpret_cast<__half2 *>(r.v)[2 * lane] = h0;
+        reinterpret_cast<__half2 *>(r.v)[2 * lane + 1] = h1;
+        W4Tail &tail = r.tail[W4Inputs::slot(place, lane / 16)];
+        if (lane % 8 == 0) tail.sum[lane / 8 % 2] = sum * -0x1p-21f;
+        if (lane % 16 == 0) tail.e = scale;
+    }
 }
 
 // Block 0 orders the picks by expert and lists the entries.  The others prepare x, counting
 // their pick's place themselves where there are few picks: one launch less; for many,
 // w4_inputs_kernel does it with the places that block 0 left (`placed`).
-__global__ void __launch_bounds__(1024) w4_group_kernel(W4Args a, int parts) {
+__global__ void __launch_bounds__(1024) w4_group_kernel(W4Args a) {
     __shared__ int32_t count[MOE_MAX_EXPERTS], sums[64];
     __shared__ int32_t bad;
     pdl_begin();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (blockIdx.x > 0) {
-        w4_inputs_of_x(a, (blockIdx.x - 1) / parts, (blockIdx.x - 1) % parts);
+        w4_inputs_of_x(a, blockIdx.x - 1);
         return;
     }
     for (int e = tid; e < MOE_MAX_EXPERTS; e += 1024) count[e] = 0;
@@ -210,9 +212,9 @@ __global__ void __launch_bounds__(1024) w4_group_kernel(W4Args a, int parts) {
     }
 }
 
-__global__ void __launch_bounds__(1024) w4_inputs_kernel(W4Args a, int parts) {
+__global__ void __launch_bounds__(1024) w4_inputs_kernel(W4Args a) {
     pdl_begin();
-    w4_inputs_of_x(a, blockIdx.x / parts, blockIdx.x % parts);
+    w4_inputs_of_x(a, blockIdx.x);
 }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0,
@@ -242,14 +244,19 @@ struct W4Item {
     }
 };
 
-// A stage holds 128 inputs: the tiles' codes and scales, and the rows.
+// A stage holds 256 inputs, the last of a unit 128 where their number is odd: the tiles' codes,
+// then their scales, then the rows, 128 inputs after the other.
 template <int G>
 struct W4Stage {
     static constexpr int kPairs = 128 / G;   // scale pairs (rows g, g + 8) per 128 inputs
-    static constexpr int kCodes = kW4Tiles * 1024, kScales = kW4Tiles * 32 * kPairs;
-    static constexpr int kBytes = kCodes + kScales + kW4Picks * (int)sizeof(W4Inputs);
-    static constexpr int kStages = (227 * 1024 / kW4Blocks - 3072) / kBytes;
-    static_assert(kStages >= 3, "stages");
+    static constexpr int kCodes = kW4Tiles * 1024, kScales = kW4Tiles * 32 * kPairs;   // of 128 inputs
+    static constexpr int kRows = kW4Picks * (int)sizeof(W4Inputs);
+    static constexpr int kBytes = 2 * (kCodes + kScales + kRows);
+    // An even number: a slot's stages then all go to the same group of warps, which so waits for a
+    // slot's next filling only after it has used the last one (a barrier tells no more than
+    // two fillings apart).  7 KB are left to other arrays.
+    static constexpr int kStages = (227 * 1024 / kW4Blocks - 8 * 1024) / kBytes / 2 * 2;
+    static_assert(kStages >= 4, "stages");
 };
 
 __device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
@@ -258,64 +265,47 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_
                  : "memory");
 }
 
-// One stage for the warp's two tiles: acc[t][r] += tile t times picks 8r .. 8r + 7.  tails[j]:
-// where in the stage the first 64 inputs' tail of pick 2q + j is (of pick 8 + 2q + j: the same
-// slot eight rows on; of the second 64 inputs: two slots on).
-template <int G, int RB>
-__device__ __forceinline__ void w4_compute(const uint8_t *stage, int warp, const int (&tails)[2], float (&acc)[2][RB][4]) {
-    using S = W4Stage<G>;
-    constexpr int kPairs = S::kPairs;
-    const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-    const uint4 *w = reinterpret_cast<const uint4 *>(stage) + warp * 2 * 64 + lane;
-    const uint32_t *sc = reinterpret_cast<const uint32_t *>(stage + S::kCodes) + (warp * 2 * 8 + g) * kPairs;
-    const W4Inputs *in = reinterpret_cast<const W4Inputs *>(stage + S::kCodes + S::kScales);
+// 128 inputs for the warp's two tiles: acc[t] += tile t times the picks.  codes, scales, x: this
+// lane's in the stage; tails[j]: the first 64 inputs' tail of pick 2q + j (the second 64 inputs'
+// lies two slots on: the slots are 64 bytes from a multiple of 64 on).
+template <int G>
+__device__ __forceinline__ void w4_compute(const uint4 *w, const uint32_t *sc, const uint4 *x, const uint8_t *base,
+                                           const int (&tails)[2], float (&acc)[2][4]) {
+    constexpr int kPairs = W4Stage<G>::kPairs;
+    float s0[2], s1[2];   // scales of rows g, g + 8
 #pragma unroll
     for (int c = 0; c < 2; ++c) {   // 64 inputs
-        asm volatile("" ::: "memory");   // their loads stay here: registers
-        uint4 b[RB][2];
+        const uint4 b[2] = {x[c * 8], x[c * 8 + 4]};
+        W4Tail tail[2];             // of this lane's columns of sums
 #pragma unroll
-        for (int r = 0; r < RB; ++r)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) b[r][h] = reinterpret_cast<const uint4 *>(in[8 * r + g].v)[c * 8 + h * 4 + q];
+        for (int j = 0; j < 2; ++j)
+            *reinterpret_cast<float4 *>(&tail[j]) = *reinterpret_cast<const float4 *>(base + (tails[j] ^ (c * 2 * (int)sizeof(W4Tail))));
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            if (RB > 1) asm volatile("" ::: "memory");
             const uint4 v = w[t * 64 + c * 32];
-            const uint8_t *tail[2];   // of this lane's columns of sums
-#pragma unroll
-            for (int j = 0; j < 2; ++j) tail[j] = stage + (tails[j] ^ (c * 2 * (int)sizeof(W4Tail)));
-            float part[RB][4];
+            float part[4];
 #pragma unroll
             for (int s = 0; s < 4; ++s) {   // 16 inputs, a matrix step
                 const uint32_t w0 = s == 0 ? v.x : s == 1 ? v.y : s == 2 ? v.z : v.w, w1 = w0 >> 8;
                 const uint32_t f[4] = {w0 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x000f000fu, w1 & 0x00f000f0u};
-#pragma unroll
-                for (int r = 0; r < RB; ++r) {
-                    const uint4 &bb = b[r][s / 2];
-                    const uint32_t b0 = s % 2 ? bb.z : bb.x, b1 = s % 2 ? bb.w : bb.y;
-                    if (s == 0 || (s == 2 && G == 32)) {   // the sum starts at -8 times the inputs' sum
-                        float z[2];
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const W4Tail *p = reinterpret_cast<const W4Tail *>(tail[j] + r * 8 * sizeof(W4Inputs));
-                            z[j] = G == 32 ? p->sum[s / 2] : p->sum[0] + p->sum[1];
-                        }
-                        mma_f16(part[r], f, b0, b1, z[0], z[1], 16.f * z[0], 16.f * z[1]);
-                    } else {
-                        mma_f16(part[r], f, b0, b1, part[r][0], part[r][1], part[r][2], part[r][3]);
-                    }
+                const uint32_t b0 = s % 2 ? b[s / 2].z : b[s / 2].x, b1 = s % 2 ? b[s / 2].w : b[s / 2].y;
+                if (s == 0 || (s == 2 && G == 32)) {   // the sum starts at -8 times the inputs' sum
+                    const float z0 = G == 32 ? tail[0].sum[s / 2] : tail[0].sum[0] + tail[0].sum[1];
+                    const float z1 = G == 32 ? tail[1].sum[s / 2] : tail[1].sum[0] + tail[1].sum[1];
+                    mma_f16(part, f, b0, b1, z0, z1, 16.f * z0, 16.f * z1);
+                } else {
+                    mma_f16(part, f, b0, b1, part[0], part[1], part[2], part[3]);
                 }
                 if (s == 3 || (s == 1 && G == 32)) {   // the end of a scale's group or of the 64 inputs
-                    const uint32_t sp = sc[t * 8 * kPairs + (c * 64 + s * 16) / G];
-#pragma unroll
-                    for (int r = 0; r < RB; ++r) {
-                        const float e0 = reinterpret_cast<const W4Tail *>(tail[0] + r * 8 * sizeof(W4Inputs))->e;
-                        const float e1 = reinterpret_cast<const W4Tail *>(tail[1] + r * 8 * sizeof(W4Inputs))->e;
-                        acc[t][r][0] = fmaf(lo_f32(sp) * e0, part[r][0], acc[t][r][0]);
-                        acc[t][r][1] = fmaf(lo_f32(sp) * e1, part[r][1], acc[t][r][1]);
-                        acc[t][r][2] = fmaf(hi_f32(sp) * e0, part[r][2], acc[t][r][2]);
-                        acc[t][r][3] = fmaf(hi_f32(sp) * e1, part[r][3], acc[t][r][3]);
+                    if (c == 0 || G < 128) {
+                        const uint32_t sp = sc[t * 8 * kPairs + (c * 64 + s * 16) / G];
+                        s0[t] = lo_f32(sp);
+                        s1[t] = hi_f32(sp);
                     }
+                    acc[t][0] = fmaf(s0[t] * tail[0].e, part[0], acc[t][0]);
+                    acc[t][1] = fmaf(s0[t] * tail[1].e, part[1], acc[t][1]);
+                    acc[t][2] = fmaf(s1[t] * tail[0].e, part[2], acc[t][2]);
+                    acc[t][3] = fmaf(s1[t] * tail[1].e, part[3], acc[t][3]);
                 }
             }
         }
@@ -324,7 +314,12 @@ __device__ __forceinline__ void w4_compute(const uint8_t *stage, int warp, const
 
 __device__ __forceinline__ float silu(float v) { return __fdiv_rn(v, 1.0f + expf(-v)); }
 
-__device__ __forceinline__ void computing_warps_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kW4Warps * 32) : "memory"); }
+// Named barriers of the computing warps: the first group's own, "sums written", "sums read".
+enum { kBarFirst = 1, kBarWritten = 2, kBarRead = 3 };
+template <int THREADS>
+__device__ __forceinline__ void bar_sync(int bar) { asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(THREADS) : "memory"); }
+template <int THREADS>
+__device__ __forceinline__ void bar_arrive(int bar) { asm volatile("bar.arrive %0, %1;" ::"r"(bar), "n"(THREADS) : "memory"); }
 
 // UP: the first product and the activation; else the second product.
 template <bool UP, int G>
@@ -334,6 +329,7 @@ __global__ void __launch_bounds__(kW4Threads, kW4Blocks) w4_product_kernel(W4Arg
     __shared__ __align__(8) uint64_t full[S::kStages], empty[S::kStages];
     __shared__ __align__(16) uint16_t acts[8][64];
     __shared__ float top[kW4Warps][8], sums[kW4Warps][8], scale[8];
+    __shared__ float others[2 * 4][kW4Warps * 32];   // the second group's sums
     __shared__ int abort_flag;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
@@ -346,52 +342,50 @@ __global__ void __launch_bounds__(kW4Threads, kW4Blocks) w4_product_kernel(W4Arg
     }
     __syncthreads();
     pdl_begin();
-    const int blocks = (UP ? a.H : a.I) / 128;   // stages of an item
+    const int blocks = (UP ? a.H : a.I) / 128, steps = (blocks + 1) / 2;   // 128 inputs, and stages, of a unit
     const int groups = (UP ? a.I / 8 : a.H / 16) / kW4Tiles;
     const int64_t units = (int64_t)*a.entries_used * groups;
-    int stage = 0;
-    uint32_t phase = 0;
-    auto next_stage = [&] {
-        if (++stage == S::kStages) {
-            stage = 0;
-            phase ^= 1;
-        }
-    };
     W4Item it;
 
-    if (warp == kW4Warps) {   // the copying warp: lane 0 the codes, 1 the scales, 2 the rows
-        int put = 0;
+    if (warp == 2 * kW4Warps) {   // the copying warp: lane 0 the codes, 1 the scales, 2 and 3 the rows
+        int put = 0, stage = 0;
+        uint32_t phase = 0;
         bool ok = true;
         for (int64_t u = blockIdx.x; ok && it.load(a, u, groups, units); u += gridDim.x) {
             const uint8_t *src;
-            uint32_t bytes, off;
-            int64_t step;
+            uint32_t bytes, off;   // of 128 inputs
+            int64_t step;          // from one stage's source to the next
             if (lane == 0) {
                 src = (UP ? a.w1 : a.w2) + it.group * blocks * S::kCodes;
-                bytes = step = S::kCodes;
+                bytes = S::kCodes;
+                step = 2 * S::kCodes;
                 off = 0;
             } else if (lane == 1) {
                 src = (UP ? a.s1 : a.s2) + it.group * blocks * S::kScales;
-                bytes = step = S::kScales;
-                off = S::kCodes;
-            } else {
-                src = reinterpret_cast<const uint8_t *>((UP ? a.xq : a.act) + it.begin);
+                bytes = S::kScales;
+                step = 2 * S::kScales;
+                off = 2 * S::kCodes;
+            } else {   // the rows of either 128 inputs
+                src = reinterpret_cast<const uint8_t *>((UP ? a.xq : a.act) + (lane == 3 ? (int64_t)a.P : 0) + it.begin);
                 bytes = it.n * (uint32_t)sizeof(W4Inputs);
-                step = (int64_t)a.P * sizeof(W4Inputs);
-                off = S::kCodes + S::kScales;
+                step = 2 * (int64_t)a.P * sizeof(W4Inputs);
+                off = 2 * (S::kCodes + S::kScales) + (lane == 3 ? S::kRows : 0);
             }
-            for (int b = 0; b < blocks; ++b) {
+            for (int b = 0; b < steps; ++b) {
                 ok = mbar_wait(smem_u32(empty + stage), phase ^ 1, &abort_flag, a.status);
                 ok = __all_sync(kAllLanes, ok);
                 if (!ok) break;
-                const uint32_t bar = smem_u32(full + stage);
-                if (lane == 0)
-                    mbar_expect_tx(bar, S::kCodes + S::kScales + it.n * (uint32_t)sizeof(W4Inputs));
+                const uint32_t bar = smem_u32(full + stage), two = 2 * b + 1 < blocks ? 2 : 1;
+                if (lane == 0) mbar_expect_tx(bar, two * (S::kCodes + S::kScales + it.n * (uint32_t)sizeof(W4Inputs)));
                 __syncwarp();
-                if (lane < 3) bulk_copy(smem_u32(stages) + stage * S::kBytes + off, src, bytes, bar);
+                if (lane < 2 + two)
+                    bulk_copy(smem_u32(stages) + stage * S::kBytes + off, src, lane < 2 ? two * bytes : bytes, bar);
                 src += step;
                 ++put;
-                next_stage();
+                if (++stage == S::kStages) {
+                    stage = 0;
+                    phase ^= 1;
+                }
             }
         }
         if (!ok) {
@@ -407,88 +401,110 @@ __global__ void __launch_bounds__(kW4Threads, kW4Blocks) w4_product_kernel(W4Arg
     }
 
     // A warp whose wait ran out (the status word then holds MOE_STATUS_TIMEOUT) goes on through
-    // the units without waiting or computing: the others may stand at the warps' barrier.
-    const int g = lane >> 2, q = lane & 3;
-    bool ok = true;
-    auto unit = [&](auto blocks_of_picks) {
-        constexpr int RB = decltype(blocks_of_picks)::value;
-        float acc[2][RB][4] = {};
+    // the units without waiting or computing: the others may stand at a barrier.
+    const int g = lane >> 2, q = lane & 3, group = warp / kW4Warps, w = warp % kW4Warps;
+    bool ok = true, written = false;
+    int put = 0;   // stages of the units so far
+    for (int64_t u = blockIdx.x; it.load(a, u, groups, units); u += gridDim.x) {
+        float acc[2][4] = {};
         int tails[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j)
-            tails[j] = S::kCodes + S::kScales + (2 * q + j) * (int)sizeof(W4Inputs) + (int)offsetof(W4Inputs, tail) +
+            tails[j] = (2 * q + j) * (int)sizeof(W4Inputs) + (int)offsetof(W4Inputs, tail) +
                        W4Inputs::slot(it.begin + 2 * q + j, 0) * (int)sizeof(W4Tail);
-        for (int b = 0; b < blocks && ok; ++b) {
+        const int first = group ^ (put & 1);   // the group takes the slots of its own parity
+        int stage = (put + first) % S::kStages;
+        uint32_t phase = (put + first) / S::kStages & 1;
+        for (int b = first; b < steps && ok; b += 2) {
             ok = mbar_wait(smem_u32(full + stage), phase, &abort_flag, a.status);
             ok = __all_sync(kAllLanes, ok);
             if (!ok) break;
-            w4_compute<G, RB>(stages + stage * S::kBytes, warp, tails, acc);
+            const uint8_t *at = stages + stage * S::kBytes;
+            const uint4 *codes = reinterpret_cast<const uint4 *>(at) + w * 2 * 64 + lane;
+            const uint32_t *sc = reinterpret_cast<const uint32_t *>(at + 2 * S::kCodes) + (w * 2 * 8 + g) * S::kPairs;
+            const uint8_t *rows = at + 2 * (S::kCodes + S::kScales);
+            const uint4 *x = reinterpret_cast<const uint4 *>(rows + g * sizeof(W4Inputs)) + q;
+            w4_compute<G>(codes, sc, x, rows, tails, acc);
+            if (2 * b + 1 < blocks)
+                w4_compute<G>(codes + S::kCodes / 16, sc + S::kScales / 4, x + S::kRows / 16, rows + S::kRows, tails, acc);
             __syncwarp();   // every lane has read the stage
             if (lane == 0) mbar_arrive(smem_u32(empty + stage));
-            next_stage();
+            stage += 2;
+            if (stage >= S::kStages) {
+                stage -= S::kStages;
+                phase ^= 1;
+            }
         }
+        put += steps;
+        // the even stages' sum plus the odd stages' (or the other way round, which is the same)
+        if (group == 1) {
+            if (written) bar_sync<kW4Warps * 64>(kBarRead);
+            written = true;
 #pragma unroll
-        for (int r = 0; r < RB; ++r) {
-            // the codes' 2^-24 (rows 0..7 of a tile) and 2^-20 (rows 8..15)
-            if constexpr (UP) {
-                // Rows 0..7 of a tile are gate rows, 8..15 the same up rows: a lane has both
-                // factors of inputs 16 warp + 8t + g of the unit's 64, of picks 2q and 2q + 1.
-                float h[2][2];   // [tile][pick]
+            for (int i = 0; i < 2 * 4; ++i) others[i][threadIdx.x - kW4Warps * 32] = acc[i / 4][i % 4];
+            bar_arrive<kW4Warps * 64>(kBarWritten);
+            continue;
+        }
+        bar_sync<kW4Warps * 64>(kBarWritten);
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
+        for (int i = 0; i < 2 * 4; ++i) acc[i / 4][i % 4] += others[i][threadIdx.x];
+        bar_arrive<kW4Warps * 64>(kBarRead);
+        // the codes' 2^-24 (rows 0..7 of a tile) and 2^-20 (rows 8..15)
+        if constexpr (UP) {
+            // Rows 0..7 of a tile are gate rows, 8..15 the same up rows: a lane has both factors
+            // of inputs 16 w + 8t + g of the unit's 64, of picks 2q and 2q + 1.
+            float h[2][2];   // [tile][pick]
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) h[t][j] = silu(acc[t][r][j] * 0x1p24f) * (acc[t][r][2 + j] * 0x1p20f);
+            for (int t = 0; t < 2; ++t)
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    float m = fmaxf(fabsf(h[0][j]), fabsf(h[1][j]));
+                for (int j = 0; j < 2; ++j) h[t][j] = silu(acc[t][j] * 0x1p24f) * (acc[t][2 + j] * 0x1p20f);
 #pragma unroll
-                    for (int o = 4; o <= 16; o <<= 1) m = fmaxf(m, __shfl_xor_sync(kAllLanes, m, o));
-                    if (g == 0) top[warp][2 * q + j] = m;
-                }
-                computing_warps_sync();
+            for (int j = 0; j < 2; ++j) {
+                float m = fmaxf(fabsf(h[0][j]), fabsf(h[1][j]));
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int c = 2 * q + j;
-                    float down, e;
-                    power_scale(fmaxf(fmaxf(top[0][c], top[1][c]), fmaxf(top[2][c], top[3][c])), down, e);
-                    const __half2 v = __floats2half2_rn(h[0][j] * down, h[1][j] * down);
-                    acts[c][16 * warp + g] = __half_as_ushort(__low2half(v));
-                    acts[c][16 * warp + 8 + g] = __half_as_ushort(__high2half(v));
-                    float sum = __low2float(v) + __high2float(v);
+                for (int o = 4; o <= 16; o <<= 1) m = fmaxf(m, __shfl_xor_sync(kAllLanes, m, o));
+                if (g == 0) top[w][2 * q + j] = m;
+            }
+            bar_sync<kW4Warps * 32>(kBarFirst);
 #pragma unroll
-                    for (int o = 4; o <= 16; o <<= 1) sum += __shfl_xor_sync(kAllLanes, sum, o);
-                    if (g == 0) sums[warp][c] = sum;
-                    if (g == 0 && warp == 0) scale[c] = e;
-                }
-                computing_warps_sync();
-                const int c = threadIdx.x >> 3, v = threadIdx.x & 7;   // pick, 8 of its 64 inputs
-                if (c < min(8, it.n - 8 * r)) {
-                    const int place = it.begin + 8 * r + c;
-                    W4Inputs &o = a.act[(int64_t)(it.i >> 1) * a.P + place];
-                    reinterpret_cast<uint4 *>(o.v)[(it.i & 1) * 8 + v] = reinterpret_cast<const uint4 *>(acts[c])[v];
-                    if (v == 0)
-                        *reinterpret_cast<float4 *>(&o.tail[W4Inputs::slot(place, it.i & 1)]) =
-                            make_float4(scale[c], (sums[0][c] + sums[1][c]) * -0x1p-21f, (sums[2][c] + sums[3][c]) * -0x1p-21f, 0.f);
-                }
-            } else {
+            for (int j = 0; j < 2; ++j) {
+                const int c = 2 * q + j;
+                float down, e;
+                power_scale(fmaxf(fmaxf(top[0][c], top[1][c]), fmaxf(top[2][c], top[3][c])), down, e);
+                const __half2 v = __floats2half2_rn(h[0][j] * down, h[1][j] * down);
+                acts[c][16 * w + g] = __half_as_ushort(__low2half(v));
+                acts[c][16 * w + 8 + g] = __half_as_ushort(__high2half(v));
+                float sum = __low2float(v) + __high2float(v);
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int c = 8 * r + 2 * q + j;
-                    if (c >= it.n) continue;
+                for (int o = 4; o <= 16; o <<= 1) sum += __shfl_xor_sync(kAllLanes, sum, o);
+                if (g == 0) sums[w][c] = sum;
+                if (g == 0 && w == 0) scale[c] = e;
+            }
+            bar_sync<kW4Warps * 32>(kBarFirst);
+            const int c = threadIdx.x >> 3, v = threadIdx.x & 7;   // pick, 8 of its 64 inputs
+            if (c < it.n) {
+                const int place = it.begin + c;
+                W4Inputs &o = a.act[(int64_t)(it.i >> 1) * a.P + place];
+                reinterpret_cast<uint4 *>(o.v)[(it.i & 1) * 8 + v] = reinterpret_cast<const uint4 *>(acts[c])[v];
+                if (v == 0)
+                    *reinterpret_cast<float4 *>(&o.tail[W4Inputs::slot(place, it.i & 1)]) =
+                        make_float4(scale[c], (sums[0][c] + sums[1][c]) * -0x1p-21f, (sums[2][c] + sums[3][c]) * -0x1p-21f, 0.f);
+            }
+        } else {
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        float *o = a.y + (int64_t)a.picks[it.begin + c] * a.H + (it.i * kW4Tiles + warp * 2 + t) * 16 + g;
-                        o[0] = acc[t][r][j] * 0x1p24f;
-                        o[8] = acc[t][r][2 + j] * 0x1p20f;
-                    }
+            for (int j = 0; j < 2; ++j) {
+                const int c = 2 * q + j;
+                if (c >= it.n) continue;
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    float *o = a.y + (int64_t)a.picks[it.begin + c] * a.H + (it.i * kW4Tiles + w * 2 + t) * 16 + g;
+                    o[0] = acc[t][j] * 0x1p24f;
+                    o[8] = acc[t][2 + j] * 0x1p20f;
                 }
             }
         }
-    };
-    for (int64_t u = blockIdx.x; it.load(a, u, groups, units); u += gridDim.x) {
-        if (it.n <= 8) unit(std::integral_constant<int, 1>{});
-        else unit(std::integral_constant<int, 2>{});
     }
+    if (written) bar_sync<kW4Warps * 64>(kBarRead);
 }
 
 // out[t] = sum over the picks, in their order, of weight * y; eight columns per thread.
@@ -499,14 +515,17 @@ __global__ void __launch_bounds__(256) w4_combine_kernel(W4Args a) {
     const int c = (int)(v - t * (a.H / 8)) * 8;
     if (t >= a.T) return;
     float o[8] = {};
-    for (int j = 0; j < a.k; ++j) {
+#pragma unroll 4
+    for (int j = 0; j < a.k; ++j) {   // (a masked pick's y and weight are read, in bounds, and not used)
         const int64_t p = t * a.k + j;
-        if (load_id(a, p) < 0) continue;
+        const bool used = load_id(a, p) >= 0;
         const float w = a.weights[p];
         const float4 *y = reinterpret_cast<const float4 *>(a.y + p * a.H + c);
         const float4 y0 = y[0], y1 = y[1];
-        o[0] = fmaf(w, y0.x, o[0]); o[1] = fmaf(w, y0.y, o[1]); o[2] = fmaf(w, y0.z, o[2]); o[3] = fmaf(w, y0.w, o[3]);
-        o[4] = fmaf(w, y1.x, o[4]); o[5] = fmaf(w, y1.y, o[5]); o[6] = fmaf(w, y1.z, o[6]); o[7] = fmaf(w, y1.w, o[7]);
+        if (used) {
+            o[0] = fmaf(w, y0.x, o[0]); o[1] = fmaf(w, y0.y, o[1]); o[2] = fmaf(w, y0.z, o[2]); o[3] = fmaf(w, y0.w, o[3]);
+            o[4] = fmaf(w, y1.x, o[4]); o[5] = fmaf(w, y1.y, o[5]); o[6] = fmaf(w, y1.z, o[6]); o[7] = fmaf(w, y1.w, o[7]);
+        }
     }
     *reinterpret_cast<uint4 *>(a.out + t * a.H + c) =
         make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7]));
@@ -743,12 +762,9 @@ int moe_forward_w4(const moe_w4_geom *g, const void *x_dev, const void *topk_ids
     a.entries = reinterpret_cast<W4Entry *>(ws + p.entries);
     a.T = (int)p.T; a.H = (int)p.H; a.E = (int)p.E; a.k = (int)p.k; a.I = (int)p.I; a.P = (int)p.P;
     a.ids64 = ids_dtype == MOE_IDS_INT64;
-    const int parts = (int)((p.H / 128 + 31) / 32);   // blocks that prepare one pick's x
-    if (p.P * parts + 1 >= ((int64_t)1 << 31)) return MOE_ERR_LIMIT;
     a.placed = p.P > kW4FewPicks;
-    cudaError_t e = launch_pdl(w4_group_kernel, dim3((unsigned)(1 + (a.placed ? 0 : p.P * parts))), dim3(1024), 0, s, a, parts);
-    if (e == cudaSuccess && a.placed)
-        e = launch_pdl(w4_inputs_kernel, dim3((unsigned)(p.P * parts)), dim3(1024), 0, s, a, parts);
+    cudaError_t e = launch_pdl(w4_group_kernel, dim3((unsigned)(1 + (a.placed ? 0 : p.P))), dim3(1024), 0, s, a);
+    if (e == cudaSuccess && a.placed) e = launch_pdl(w4_inputs_kernel, dim3((unsigned)p.P), dim3(1024), 0, s, a);
     if (e == cudaSuccess && p.T > 0) {
         const int64_t entries = (p.P < p.E ? p.P : p.E) + p.P / kW4Picks;   // at most
         e = launch_product<true>(a, p.G, entries * (p.I / 8 / kW4Tiles), s);
