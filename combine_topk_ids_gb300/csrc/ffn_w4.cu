@@ -62,9 +62,10 @@ struct W4Plan {
 
 // One run of up to kW4Picks picks of one expert.  An expert's runs follow each other; they work
 // through the same weights at the same time (W4Item).
-struct W4Entry {
+struct __align__(16) W4Entry {
     int32_t expert, first, runs, begin, end, pad[3];   // the expert's first entry and their number; its places
 };
+static_assert(sizeof(W4Entry) == 32, "W4Item reads the first four at once");
 
 struct W4Args {
     const uint16_t *x;
@@ -84,6 +85,10 @@ __device__ __forceinline__ int load_id(const W4Args &a, int64_t p) {
     const int64_t v = a.ids64 ? static_cast<const int64_t *>(a.ids)[p] : static_cast<const int32_t *>(a.ids)[p];
     return v >= 0 && v < a.E ? (int)v : v == -1 ? -1 : -2;
 }
+
+// The next kernel of the call may be launched: it waits for this one before it touches what
+// this one writes.
+__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // 1 / e and e for the largest magnitude m of 64 inputs.
 __device__ __forceinline__ void power_scale(float m, float &down, float &e) {
@@ -137,6 +142,7 @@ __global__ void __launch_bounds__(1024) w4_group_kernel(W4Args a) {
     __shared__ int32_t count[MOE_MAX_EXPERTS], sums[64];
     __shared__ int32_t bad;
     pdl_begin();
+    pdl_trigger();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (blockIdx.x > 0) {
         w4_inputs_of_x(a, blockIdx.x - 1);
@@ -231,15 +237,26 @@ struct W4Item {
     int64_t group;       // of tiles, in the matrix
     int i, begin, n;     // of tiles, in the expert; the picks a.picks[begin .. begin + n)
 
+    // EARLY: before the dependency wait, past the L1.
+    template <bool EARLY = false>
     __device__ __forceinline__ bool load(const W4Args &a, int64_t u, int groups, int64_t units) {
         if (u >= units) return false;
-        const W4Entry first = a.entries[u / groups];
-        const int64_t local = u - (int64_t)first.first * groups;   // in the expert's entries
-        i = (int)(local / first.runs);
-        const W4Entry e = a.entries[first.first + (int)(local - (int64_t)i * first.runs)];
-        group = (int64_t)e.expert * groups + i;
-        begin = e.begin;
-        n = e.end - e.begin;
+        auto get = [](const int4 *p) { return EARLY ? __ldcg(p) : *p; };
+        const int entry = units < ((int64_t)1 << 31) ? (int)u / groups : (int)(u / groups);
+        const int4 *e = reinterpret_cast<const int4 *>(a.entries + entry);
+        int4 x = get(e);            // expert, first, runs, begin
+        int4 y = get(e + 1);        // end
+        i = (int)(u - (int64_t)entry * groups);
+        if (x.z > 1) {
+            const int local = (int)(u - (int64_t)x.y * groups);   // in the expert's entries
+            i = local / x.z;
+            e = reinterpret_cast<const int4 *>(a.entries + x.y + (local - i * x.z));
+            x = get(e);
+            y = get(e + 1);
+        }
+        group = (int64_t)x.x * groups + i;
+        begin = x.w;
+        n = y.x - begin;
         return true;
     }
 };
@@ -341,17 +358,22 @@ __global__ void __launch_bounds__(kW4Threads, kW4Blocks) w4_product_kernel(W4Arg
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
-    pdl_begin();
+    // The first product lets the second one start as blocks of it end: that one's copying warp
+    // then fetches weights, which depend on the grouping alone, before it waits for the activation.
+    if (UP) pdl_begin();
+    if (UP) pdl_trigger();
     const int blocks = (UP ? a.H : a.I) / 128, steps = (blocks + 1) / 2;   // 128 inputs, and stages, of a unit
     const int groups = (UP ? a.I / 8 : a.H / 16) / kW4Tiles;
-    const int64_t units = (int64_t)*a.entries_used * groups;
+    const int entries = __ldcg(a.entries_used);
+    const int64_t units = (int64_t)entries * groups;
     W4Item it;
 
     if (warp == 2 * kW4Warps) {   // the copying warp: lane 0 the codes, 1 the scales, 2 and 3 the rows
         int put = 0, stage = 0;
         uint32_t phase = 0;
         bool ok = true;
-        for (int64_t u = blockIdx.x; ok && it.load(a, u, groups, units); u += gridDim.x) {
+        bool have = it.load<!UP>(a, blockIdx.x, groups, units);
+        for (int64_t u = blockIdx.x; ok && have; u += gridDim.x, have = it.load(a, u, groups, units)) {
             const uint8_t *src;
             uint32_t bytes, off;   // of 128 inputs
             int64_t step;          // from one stage's source to the next
@@ -371,14 +393,28 @@ __global__ void __launch_bounds__(kW4Threads, kW4Blocks) w4_product_kernel(W4Arg
                 step = 2 * (int64_t)a.P * sizeof(W4Inputs);
                 off = 2 * (S::kCodes + S::kScales) + (lane == 3 ? S::kRows : 0);
             }
+            int ahead = 0;   // stages of this unit whose weights are under way already
+            if (!UP && put == 0) {
+                for (; ahead < min(steps, S::kStages); ++ahead) {
+                    const uint32_t bar = smem_u32(full + ahead), two = 2 * ahead + 1 < blocks ? 2 : 1;
+                    if (lane == 0) mbar_expect_tx(bar, two * (S::kCodes + S::kScales + it.n * (uint32_t)sizeof(W4Inputs)));
+                    __syncwarp();
+                    if (lane < 2)
+                        bulk_copy(smem_u32(stages) + ahead * S::kBytes + off, src + ahead * step, two * bytes, bar);
+                }
+                pdl_begin();
+            }
             for (int b = 0; b < steps; ++b) {
                 ok = mbar_wait(smem_u32(empty + stage), phase ^ 1, &abort_flag, a.status);
                 ok = __all_sync(kAllLanes, ok);
                 if (!ok) break;
                 const uint32_t bar = smem_u32(full + stage), two = 2 * b + 1 < blocks ? 2 : 1;
-                if (lane == 0) mbar_expect_tx(bar, two * (S::kCodes + S::kScales + it.n * (uint32_t)sizeof(W4Inputs)));
-                __syncwarp();
-                if (lane < 2 + two)
+                if (b >= ahead) {
+                    if (lane == 0)
+                        mbar_expect_tx(bar, two * (S::kCodes + S::kScales + it.n * (uint32_t)sizeof(W4Inputs)));
+                    __syncwarp();
+                }
+                if (lane < 2 + two && (lane >= 2 || b >= ahead))
                     bulk_copy(smem_u32(stages) + stage * S::kBytes + off, src, lane < 2 ? two * bytes : bytes, bar);
                 src += step;
                 ++put;
@@ -388,6 +424,7 @@ __global__ void __launch_bounds__(kW4Threads, kW4Blocks) w4_product_kernel(W4Arg
                 }
             }
         }
+        if (!UP && put == 0) pdl_begin();   // no unit: the kernel still ends after the one before
         if (!ok) {
             // gave up: the copies under way may not outlive the block, so each stage's gets one
             // more bounded wait (the status word already holds MOE_STATUS_TIMEOUT)
@@ -402,6 +439,7 @@ __global__ void __launch_bounds__(kW4Threads, kW4Blocks) w4_product_kernel(W4Arg
 
     // A warp whose wait ran out (the status word then holds MOE_STATUS_TIMEOUT) goes on through
     // the units without waiting or computing: the others may stand at a barrier.
+    if (!UP) pdl_begin();
     const int g = lane >> 2, q = lane & 3, group = warp / kW4Warps, w = warp % kW4Warps;
     bool ok = true, written = false;
     int put = 0;   // stages of the units so far
@@ -507,13 +545,12 @@ __global__ void __launch_bounds__(kW4Threads, kW4Blocks) w4_product_kernel(W4Arg
     if (written) bar_sync<kW4Warps * 64>(kBarRead);
 }
 
-// out[t] = sum over the picks, in their order, of weight * y; eight columns per thread.
-__global__ void __launch_bounds__(256) w4_combine_kernel(W4Args a) {
+// out[t] = sum over the picks, in their order, of weight * y; a block to 1024 columns of a token.
+__global__ void __launch_bounds__(128) w4_combine_kernel(W4Args a) {
     pdl_begin();
-    const int64_t v = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t t = v / (a.H / 8);
-    const int c = (int)(v - t * (a.H / 8)) * 8;
-    if (t >= a.T) return;
+    const int64_t t = blockIdx.x;
+    const int c = blockIdx.y * 1024 + threadIdx.x * 8;
+    if (c >= a.H) return;
     float o[8] = {};
 #pragma unroll 4
     for (int j = 0; j < a.k; ++j) {   // (a masked pick's y and weight are read, in bounds, and not used)
@@ -770,7 +807,7 @@ int moe_forward_w4(const moe_w4_geom *g, const void *x_dev, const void *topk_ids
         e = launch_product<true>(a, p.G, entries * (p.I / 8 / kW4Tiles), s);
         if (e == cudaSuccess) e = launch_product<false>(a, p.G, entries * (p.H / 16 / kW4Tiles), s);
         if (e == cudaSuccess)
-            e = launch_pdl(w4_combine_kernel, dim3(blocks256(p.T * (p.H / 8))), dim3(256), 0, s, a);
+            e = launch_pdl(w4_combine_kernel, dim3((unsigned)p.T, (unsigned)((p.H + 1023) / 1024)), dim3(128), 0, s, a);
     }
     return status_of(e);
 }
