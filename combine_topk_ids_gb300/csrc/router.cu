@@ -5,6 +5,12 @@
 // One warp per token; lane l holds the EPL consecutive experts from l * EPL on, so that the
 // lowest lane with a value holds its lowest expert.  Keys are compared as 32-bit integers
 // whose order is that of the floats; 0 is "absent".
+//
+// The logits are read once and little is written, but a token's selection takes a few hundred
+// instructions for E = 256: the instruction issue bounds large batches, the launch small ones.
+// So the k largest keys are not taken out one by one: the k-th largest of the lanes' maxima is
+// a bound that few keys reach (about 11 for k = 8 of 256); these are put together in shared
+// memory and ranked against each other, one to a lane.
 #include "block_common.cuh"
 
 namespace moe {
@@ -20,6 +26,7 @@ struct RouterArgs {
     void *dlogits;
     int64_t stride;          // of logits, in elements
     int T, E, k, sigmoid, groups, top_groups, pair, renorm, f32, ids64, by_logit;
+    int lanes_per_group;     // where a group is a power of two of whole lanes, else 0
     float scale;
 };
 
@@ -33,17 +40,58 @@ __device__ __forceinline__ float of_key(uint32_t o) {
     return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
 }
 
-// Logit of expert e as float32, -infinity beyond the last expert and for NaN; +infinity
-// counts as the largest finite value.
-__device__ __forceinline__ float load_logit(const RouterArgs &a, int64_t t, int e) {
+// A lane's logits as float32: -infinity beyond the last expert and for NaN; +infinity counts as
+// the largest finite value.  VEC: 16-byte (8-byte) loads; the lanes' experts then all exist or
+// none of them does.
+template <int EPL, bool VEC>
+__device__ __forceinline__ void load_logits(const RouterArgs &a, int64_t t, int first, float (&l)[EPL]) {
     const float none = -__int_as_float(0x7f800000);
-    if (e >= a.E) return none;
-    const float v = a.f32 ? static_cast<const float *>(a.logits)[t * a.stride + e]
-                          : __bfloat162float(static_cast<const __nv_bfloat16 *>(a.logits)[t * a.stride + e]);
-    return v != v ? none : fminf(v, 3.402823466e38f);
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) l[j] = none;
+    if (VEC) {
+        if (first < a.E) {
+            if (a.f32) {
+                const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(a.logits) + t * a.stride + first);
+#pragma unroll
+                for (int j = 0; j + 4 <= EPL; j += 4) {
+                    const float4 v = p[j / 4];
+                    l[j] = v.x; l[j + 1] = v.y; l[j + 2] = v.z; l[j + 3] = v.w;
+                }
+            } else {
+                const uint2 *p = reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(a.logits) + t * a.stride + first);
+#pragma unroll
+                for (int j = 0; j + 4 <= EPL; j += 4) {
+                    const uint2 v = p[j / 4];
+                    l[j] = lo_f32(v.x); l[j + 1] = hi_f32(v.x); l[j + 2] = lo_f32(v.y); l[j + 3] = hi_f32(v.y);
+                }
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < EPL; ++j)
+            if (first + j < a.E)
+                l[j] = a.f32 ? static_cast<const float *>(a.logits)[t * a.stride + first + j]
+                             : __bfloat162float(static_cast<const __nv_bfloat16 *>(a.logits)[t * a.stride + first + j]);
+    }
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) l[j] = l[j] != l[j] ? none : fminf(l[j], 3.402823466e38f);
 }
 
-__device__ __forceinline__ float sigmoid(float v) { return __fdiv_rn(1.0f, 1.0f + expf(-v)); }
+// 1 / (1 + e^-v), the reciprocal to within 1 ulp.
+__device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.0f, 1.0f + expf(-v)); }
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAllLanes, v, o));
+    return v;
+}
+template <int EPL>
+__device__ __forceinline__ float row_max(const float (&l)[EPL]) {
+    float m = -3.402823466e38f;   // the lowest finite value is a logit like any other
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) m = fmaxf(m, l[j]);
+    return warp_max(m);
+}
 
 // Scores of a lane's experts.  Softmax over the whole row, with the row's maximum taken out
 // before the exponential; a row with no expert has all scores 0.
@@ -54,106 +102,201 @@ __device__ __forceinline__ void score_row(const RouterArgs &a, const float (&l)[
         for (int j = 0; j < EPL; ++j) s[j] = sigmoid(l[j]);
         return;
     }
-    float m = -3.402823466e38f;   // the lowest finite value is a logit like any other
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) m = fmaxf(m, l[j]);
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAllLanes, m, o));
+    const float m = row_max<EPL>(l);
     float z = 0.f;
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
         s[j] = expf(l[j] - m);
         z += s[j];
     }
-    z = fmaxf(warp_sum(z), 1e-38f);
+    z = __fdiv_rn(1.0f, fmaxf(warp_sum(z), 1e-38f));
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) s[j] = __fdiv_rn(s[j], z);
+    for (int j = 0; j < EPL; ++j) s[j] *= z;
 }
 
+// Takes the keys of experts outside the top_groups best groups out (0).
 template <int EPL>
+__device__ __forceinline__ void keep_groups(const RouterArgs &a, int lane, uint32_t (&key)[EPL], uint32_t *keys) {
+    const int size = a.E / a.groups;
+    uint32_t first = 0, second = 0;   // the group's two largest keys
+    if (a.lanes_per_group > 0) {      // whole lanes, a power of two of them: exchanges among these
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+            second = max(second, min(first, key[j]));
+            first = max(first, key[j]);
+        }
+        for (int o = 1; o < a.lanes_per_group; o <<= 1) {
+            const uint32_t f = __shfl_xor_sync(kAllLanes, first, o), s = __shfl_xor_sync(kAllLanes, second, o);
+            second = max(max(second, s), min(first, f));
+            first = max(first, f);
+        }
+        const uint32_t score = a.pair && second != 0 ? key_of(__fadd_rn(of_key(first), of_key(second))) : first;
+        const int mine = lane / a.lanes_per_group;
+        int rank = 0;
+        for (int g = 0; g < a.groups; ++g) {
+            const uint32_t other = __shfl_sync(kAllLanes, score, g * a.lanes_per_group);
+            rank += other > score || (other == score && g < mine);
+        }
+        if (rank >= a.top_groups)
+#pragma unroll
+            for (int j = 0; j < EPL; ++j) key[j] = 0;
+        return;
+    }
+    // any other size: through shared memory, a lane to each group
+#pragma unroll
+    for (int j = 0; j < EPL; ++j)
+        if (lane * EPL + j < a.E) keys[lane * EPL + j] = key[j];
+    __syncwarp();
+    if (lane < a.groups)
+        for (int i = 0; i < size; ++i) {
+            const uint32_t v = keys[lane * size + i];
+            second = max(second, min(first, v));
+            first = max(first, v);
+        }
+    __syncwarp();
+    const uint32_t score = a.pair && second != 0 ? key_of(__fadd_rn(of_key(first), of_key(second))) : first;
+    int rank = 0;
+    for (int g = 0; g < a.groups; ++g) {
+        const uint32_t other = __shfl_sync(kAllLanes, score, g);
+        rank += other > score || (other == score && g < lane);
+    }
+    const uint32_t kept = __ballot_sync(kAllLanes, lane < a.groups && rank < a.top_groups);
+    int g = lane * EPL / size, rest = lane * EPL - g * size;   // of the lane's first expert
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+        if (!((kept >> (g & 31)) & 1)) key[j] = 0;
+        if (++rest == size) {
+            rest = 0;
+            ++g;
+        }
+    }
+}
+
+// A token's room in shared memory: the keys (keep_groups) or the candidates.
+__host__ __device__ constexpr int room_of(int E) { return E > 96 ? E : 96; }
+
+template <int EPL, bool VEC>
 __global__ void __launch_bounds__(kWarps * 32) route_topk_kernel(RouterArgs a) {
-    extern __shared__ uint32_t shared_keys[];   // [kWarps][E] with groups
+    extern __shared__ __align__(16) uint32_t rooms[];   // [kWarps][room_of(E)]
     pdl_begin();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t t = (int64_t)blockIdx.x * kWarps + warp;
     if (t >= a.T) return;
-    float l[EPL], s[EPL];
+    uint32_t *room = rooms + warp * room_of(a.E);
+    float l[EPL];
     uint32_t key[EPL];
+    load_logits<EPL, VEC>(a, t, lane * EPL, l);
+    // s: the score, or the logit where the score is computed for the picks alone
+    float m = 0.f;
+    if (a.by_logit) {
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) l[j] = load_logit(a, t, lane * EPL + j);
-    score_row<EPL>(a, l, s);
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) {
-        const int e = lane * EPL + j;
-        const float b = a.bias && e < a.E ? a.bias[e] : 0.f;
-        key[j] = key_of(a.by_logit ? l[j] : __fadd_rn(s[j], b));
-        if (key_of(l[j]) == 0) key[j] = 0;
+        for (int j = 0; j < EPL; ++j) key[j] = key_of(l[j]);
+        if (!a.sigmoid) m = row_max<EPL>(l);
     }
-
-    if (a.groups > 1) {   // lane g takes group g's score and its rank among the groups
-        uint32_t *keys = shared_keys + warp * a.E;
+    float z = 1.f;   // what the picks' scores are divided by, before their own sum
+    if (a.by_logit && !a.sigmoid && !a.renorm) {
+        z = 0.f;
 #pragma unroll
-        for (int j = 0; j < EPL; ++j)
-            if (lane * EPL + j < a.E) keys[lane * EPL + j] = key[j];
-        __syncwarp();
-        const int size = a.E / a.groups;
-        uint32_t score = 0;
-        if (lane < a.groups) {
-            uint32_t first = 0, second = 0;
-            for (int i = 0; i < size; ++i) {
-                const uint32_t v = keys[lane * size + i];
-                second = max(second, min(first, v));
-                first = max(first, v);
-            }
-            score = a.pair && second != 0 ? key_of(__fadd_rn(of_key(first), of_key(second))) : first;
-        }
-        int rank = 0;
-        for (int g = 0; g < a.groups; ++g) {
-            const uint32_t other = __shfl_sync(kAllLanes, score, g);
-            rank += other > score || (other == score && g < lane);
-        }
-        const uint32_t kept = __ballot_sync(kAllLanes, lane < a.groups && rank < a.top_groups);
-#pragma unroll
-        for (int j = 0; j < EPL; ++j)
-            if (lane * EPL + j < a.E && !((kept >> ((lane * EPL + j) / size)) & 1)) key[j] = 0;
+        for (int j = 0; j < EPL; ++j) z += expf(l[j] - m);
+        z = fmaxf(warp_sum(z), 1e-38f);
     }
+    if (!a.by_logit) {
+        float s[EPL];
+        score_row<EPL>(a, l, s);
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+            const int e = lane * EPL + j;
+            const float b = a.bias && e < a.E ? __ldg(a.bias + e) : 0.f;
+            key[j] = key_of(l[j]) ? key_of(__fadd_rn(s[j], b)) : 0;
+            l[j] = s[j];
+        }
+    }
+    if (a.groups > 1) keep_groups<EPL>(a, lane, key, room);
 
-    // k times the largest key; lane j keeps pick j
+    // the bound: the k-th largest of the lanes' maxima (1, every key there is, if there are fewer)
     uint32_t best = 0;
 #pragma unroll
     for (int j = 0; j < EPL; ++j) best = max(best, key[j]);
-    int id = -1;
-    float w = 0.f;
+    uint32_t bound = 1, rest = best;
     for (int i = 0; i < a.k; ++i) {
-        const uint32_t top = __reduce_max_sync(kAllLanes, best);
+        const uint32_t top = __reduce_max_sync(kAllLanes, rest);
+        bound = max(top, 1u);
         if (top == 0) break;
-        const int owner = __ffs(__ballot_sync(kAllLanes, best == top)) - 1;
-        int at = -1;
-        float sc = 0.f;
-        if (lane == owner) {
-            best = 0;
+        if (rest == top) rest = 0;   // all of its lanes: the bound only gets lower
+    }
+    int mine = 0;
 #pragma unroll
-            for (int j = 0; j < EPL; ++j) {
-                if (at < 0 && key[j] == top) {
-                    at = lane * EPL + j;
-                    sc = s[j];
-                    key[j] = 0;
+    for (int j = 0; j < EPL; ++j) mine += key[j] >= bound;
+    int at = mine;   // candidates up to this lane's last
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(kAllLanes, at, o);
+        if (lane >= o) at += v;
+    }
+    const int n = __shfl_sync(kAllLanes, at, 31);
+    int id = -1, rank = lane;
+    float w = 0.f;
+    if (n <= 32) {
+        // in the experts' order into shared memory; a lane's candidate comes behind those with a
+        // larger key, and behind equal ones before it
+        at -= mine;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j)
+            if (key[j] >= bound) {
+                room[at] = key[j];
+                room[32 + at] = __float_as_uint(l[j]);
+                room[64 + at] = lane * EPL + j;
+                ++at;
+            }
+        __syncwarp();
+        uint32_t own = 0;
+        if (lane < n) {
+            own = room[lane];
+            w = __uint_as_float(room[32 + lane]);
+            id = (int)room[64 + lane];
+        }
+        int before = 0;
+        for (int i = 0; i < n; ++i) {
+            const uint32_t other = __shfl_sync(kAllLanes, own, i);
+            before += other > own || (other == own && i < lane);
+        }
+        rank = before;   // lanes without a candidate (key 0) come last, in their own order
+        if (lane >= n) rank = lane;
+        if (rank >= a.k) w = 0.f;
+    } else {   // many equal keys, or k near the number of lanes: one by one, pick i to lane i
+        for (int i = 0; i < a.k; ++i) {
+            const uint32_t top = __reduce_max_sync(kAllLanes, best);
+            if (top == 0) break;
+            const int owner = __ffs(__ballot_sync(kAllLanes, best == top)) - 1;
+            int which = -1;
+            float sc = 0.f;
+            if (lane == owner) {
+                best = 0;
+#pragma unroll
+                for (int j = 0; j < EPL; ++j) {
+                    if (which < 0 && key[j] == top) {
+                        which = lane * EPL + j;
+                        sc = l[j];
+                        key[j] = 0;
+                    }
+                    best = max(best, key[j]);
                 }
-                best = max(best, key[j]);
+            }
+            which = __shfl_sync(kAllLanes, which, owner);
+            sc = __shfl_sync(kAllLanes, sc, owner);
+            if (lane == i) {
+                id = which;
+                w = sc;
             }
         }
-        at = __shfl_sync(kAllLanes, at, owner);
-        sc = __shfl_sync(kAllLanes, sc, owner);
-        if (lane == i) {
-            id = at;
-            w = sc;
-        }
     }
+    const bool picked = id >= 0 && rank < a.k;
+    if (a.by_logit) w = !picked ? 0.f : a.sigmoid ? sigmoid(w) : __fdiv_rn(expf(w - m), z);
     if (a.renorm) w = __fdiv_rn(w, fmaxf(warp_sum(w), 1e-38f));
-    if (lane < a.k) {
-        const int64_t o = t * a.k + lane;
-        if (a.ids64) static_cast<int64_t *>(a.ids)[o] = id;
-        else static_cast<int32_t *>(a.ids)[o] = id;
+    if (rank < a.k) {
+        const int64_t o = t * a.k + rank;
+        if (a.ids64) static_cast<int64_t *>(a.ids)[o] = picked ? id : -1;
+        else static_cast<int32_t *>(a.ids)[o] = picked ? id : -1;
         a.weights[o] = w * a.scale;
     }
 }
@@ -161,19 +304,14 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_kernel(RouterArgs a) {
 // With p the picked scores, z their sum and g = scale * dweights:
 //   ds = g, or (g - sum(g p)/z)/z where renormalised (0 outside the picks);
 //   dlogit = ds s (1 - s) for the sigmoid, s (ds - sum(ds s)) for the softmax.
-template <int EPL>
+template <int EPL, bool VEC>
 __global__ void __launch_bounds__(kWarps * 32) route_topk_backward_kernel(RouterArgs a) {
+    extern __shared__ __align__(16) uint32_t rooms[];   // [kWarps][32 * EPL]
     pdl_begin();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t t = (int64_t)blockIdx.x * kWarps + warp;
     if (t >= a.T) return;
-    float l[EPL], s[EPL], d[EPL];
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) {
-        l[j] = load_logit(a, t, lane * EPL + j);
-        d[j] = 0.f;
-    }
-    score_row<EPL>(a, l, s);
+    float *room = reinterpret_cast<float *>(rooms) + warp * 32 * EPL;
     int id = -1;
     float g = 0.f;
     if (lane < a.k) {
@@ -184,28 +322,35 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_backward_kernel(Router
             g = a.weights[o] * a.scale;
         }
     }
+    float l[EPL], s[EPL], d[EPL];
+    load_logits<EPL, VEC>(a, t, lane * EPL, l);
+    score_row<EPL>(a, l, s);
     if (a.renorm) {
-        float p = 0.f;   // the score of this lane's pick
-        for (int i = 0; i < a.k; ++i) {
-            const int e = __shfl_sync(kAllLanes, id, i);
-            float v = 0.f;
 #pragma unroll
-            for (int j = 0; j < EPL; ++j)
-                if (e == lane * EPL + j) v = s[j];
-            v = e >= 0 ? __shfl_sync(kAllLanes, v, e / EPL) : 0.f;
-            if (lane == i) p = v;
-        }
+        for (int j = 0; j < EPL; ++j) room[lane * EPL + j] = s[j];
+        __syncwarp();
+        const float p = id >= 0 ? room[id] : 0.f;   // the score of this lane's pick
+        __syncwarp();
         const float z = fmaxf(warp_sum(p), 1e-38f);
         const float along = __fdiv_rn(warp_sum(g * p), z);
         g = id >= 0 ? __fdiv_rn(g - along, z) : 0.f;
     }
-    for (int i = 0; i < a.k; ++i) {
-        const int e = __shfl_sync(kAllLanes, id, i);
-        const float v = __shfl_sync(kAllLanes, g, i);
+    // the picks' gradients to the experts' lanes; picks of one expert add up in their order
 #pragma unroll
-        for (int j = 0; j < EPL; ++j)
-            if (e == lane * EPL + j) d[j] += v;
+    for (int j = 0; j < EPL; ++j) room[lane * EPL + j] = 0.f;
+    __syncwarp();
+    const unsigned same = __match_any_sync(kAllLanes, id);
+    if (__all_sync(kAllLanes, id < 0 || __popc(same) == 1)) {
+        if (id >= 0) room[id] = g;
+    } else {
+        for (int i = 0; i < a.k; ++i) {
+            if (lane == i && id >= 0) room[id] += g;
+            __syncwarp();
+        }
     }
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) d[j] = room[lane * EPL + j];
     if (a.sigmoid) {
 #pragma unroll
         for (int j = 0; j < EPL; ++j) d[j] = d[j] * s[j] * (1.0f - s[j]);
@@ -217,12 +362,26 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_backward_kernel(Router
 #pragma unroll
         for (int j = 0; j < EPL; ++j) d[j] = s[j] * (d[j] - along);
     }
+    const int first = lane * EPL;
+    if (VEC) {
+        if (first >= a.E) return;
+        if (a.f32) {
+            float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(a.dlogits) + t * a.E + first);
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) {
-        const int e = lane * EPL + j;
-        if (e >= a.E) continue;
-        if (a.f32) static_cast<float *>(a.dlogits)[t * a.E + e] = d[j];
-        else static_cast<__nv_bfloat16 *>(a.dlogits)[t * a.E + e] = __float2bfloat16_rn(d[j]);
+            for (int j = 0; j + 4 <= EPL; j += 4) o[j / 4] = make_float4(d[j], d[j + 1], d[j + 2], d[j + 3]);
+        } else {
+            uint2 *o = reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.dlogits) + t * a.E + first);
+#pragma unroll
+            for (int j = 0; j + 4 <= EPL; j += 4) o[j / 4] = make_uint2(pack_bf16(d[j], d[j + 1]), pack_bf16(d[j + 2], d[j + 3]));
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+            const int e = first + j;
+            if (e >= a.E) continue;
+            if (a.f32) static_cast<float *>(a.dlogits)[t * a.E + e] = d[j];
+            else static_cast<__nv_bfloat16 *>(a.dlogits)[t * a.E + e] = __float2bfloat16_rn(d[j]);
+        }
     }
 }
 
@@ -260,19 +419,34 @@ RouterArgs router_args(const moe_router *r, int32_t T, const void *logits, const
     a.ids64 = ids_dtype == MOE_IDS_INT64;
     a.by_logit = !bias && (r->groups == 1 || !a.pair);
     a.scale = r->scale;
+    int epl = 1;
+    while (32 * epl < a.E) epl *= 2;
+    const int size = a.E / a.groups, lanes = size / epl;
+    a.lanes_per_group = size % epl == 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
     return a;
 }
 
-// Calls f with the number of experts per lane as a compile-time power of two.
+// Calls f with the number of experts per lane as a compile-time power of two, and whether the
+// lanes' experts can be read (and, for the gradient, written) together: four of them aligned,
+// and every lane's all there or none.
 template <typename F>
-cudaError_t with_epl(int E, F &&f) {
-    if (E <= 32) return f(std::integral_constant<int, 1>{});
-    if (E <= 64) return f(std::integral_constant<int, 2>{});
-    if (E <= 128) return f(std::integral_constant<int, 4>{});
-    if (E <= 256) return f(std::integral_constant<int, 8>{});
-    if (E <= 512) return f(std::integral_constant<int, 16>{});
-    if (E <= 1024) return f(std::integral_constant<int, 32>{});
-    return f(std::integral_constant<int, 64>{});
+cudaError_t with_epl(const RouterArgs &a, F &&f) {
+    const size_t b = a.f32 ? 16 : 8;
+    auto vec = [&](auto epl) {
+        constexpr int n = decltype(epl)::value;
+        if constexpr (n >= 4) {
+            if (a.E % n == 0 && a.stride % 4 == 0 && is_aligned(a.logits, b) && is_aligned(a.dlogits, b))
+                return f(epl, std::true_type{});
+        }
+        return f(epl, std::false_type{});
+    };
+    if (a.E <= 32) return vec(std::integral_constant<int, 1>{});
+    if (a.E <= 64) return vec(std::integral_constant<int, 2>{});
+    if (a.E <= 128) return vec(std::integral_constant<int, 4>{});
+    if (a.E <= 256) return vec(std::integral_constant<int, 8>{});
+    if (a.E <= 512) return vec(std::integral_constant<int, 16>{});
+    if (a.E <= 1024) return vec(std::integral_constant<int, 32>{});
+    return vec(std::integral_constant<int, 64>{});
 }
 
 }  // namespace
@@ -294,10 +468,11 @@ int moe_route_topk(const moe_router *r, int32_t num_tokens, const void *logits_d
     if (num_tokens == 0) return MOE_OK;
     const RouterArgs a = router_args(r, num_tokens, logits_dev, bias_dev, topk_ids_dev, ids_dtype,
                                      topk_weights_dev, nullptr);
-    const size_t smem = a.groups > 1 ? (size_t)kWarps * a.E * 4 : 0;   // at most 32 KB
-    return status_of(with_epl(a.E, [&](auto epl) {
-        return launch_pdl(route_topk_kernel<decltype(epl)::value>, dim3((a.T + kWarps - 1) / kWarps),
-                          dim3(kWarps * 32), smem, static_cast<cudaStream_t>(stream), a);
+    const size_t smem = (size_t)kWarps * room_of(a.E) * 4;   // at most 32 KB
+    return status_of(with_epl(a, [&](auto epl, auto vec) {
+        return launch_pdl(route_topk_kernel<decltype(epl)::value, decltype(vec)::value>,
+                          dim3((a.T + kWarps - 1) / kWarps), dim3(kWarps * 32), smem,
+                          static_cast<cudaStream_t>(stream), a);
     }));
 }
 
@@ -315,9 +490,10 @@ int moe_route_topk_backward(const moe_router *r, int32_t num_tokens, const void 
     if (num_tokens == 0) return MOE_OK;
     const RouterArgs a = router_args(r, num_tokens, logits_dev, nullptr, topk_ids_dev, ids_dtype, dweights_dev,
                                      dlogits_dev);
-    return status_of(with_epl(a.E, [&](auto epl) {
-        return launch_pdl(route_topk_backward_kernel<decltype(epl)::value>, dim3((a.T + kWarps - 1) / kWarps),
-                          dim3(kWarps * 32), 0, static_cast<cudaStream_t>(stream), a);
+    return status_of(with_epl(a, [&](auto epl, auto vec) {
+        constexpr int n = decltype(epl)::value;
+        return launch_pdl(route_topk_backward_kernel<n, decltype(vec)::value>, dim3((a.T + kWarps - 1) / kWarps),
+                          dim3(kWarps * 32), (size_t)kWarps * 32 * n * 4, static_cast<cudaStream_t>(stream), a);
     }));
 }
 
