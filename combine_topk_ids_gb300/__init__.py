@@ -74,6 +74,7 @@ def lib():
         L.moe_workspace_size.argtypes = [G, sz]
         L.moe_expert_out_size.argtypes = [G, sz]
         L.moe_dispatch.argtypes = [G, _P, _P, ctypes.c_int, _P, _P, _P, ctypes.c_size_t, H, _P]
+        L.moe_dispatch_fp8.argtypes = [G, _P, _P, _P, ctypes.c_int, _P, _P, _P, ctypes.c_size_t, H, _P]
         L.moe_prepare_weights.argtypes = [G, _P, _P, _P]
         L.moe_expert_ffn.argtypes = [H, _P, _P, _P, _P]
         L.moe_combine.argtypes = [H, _P, _P, _P, _P]
@@ -92,7 +93,7 @@ def lib():
         L.moe_strerror.argtypes = [ctypes.c_int]
         L.moe_strerror.restype = ctypes.c_char_p
         for f in ("moe_workspace_size", "moe_expert_out_size", "moe_dispatch",
-                  "moe_prepare_weights", "moe_expert_ffn", "moe_combine", "moe_get_status",
+                  "moe_dispatch_fp8", "moe_prepare_weights", "moe_expert_ffn", "moe_combine", "moe_get_status",
                   "moe_forward_host", "moe_quantize_weights_fp8", "moe_prepare_weights_fp8",
                   "moe_expert_ffn_fp8"):
             getattr(L, f).restype = ctypes.c_int
@@ -156,6 +157,18 @@ def moe_dispatch(g, x, topk_ids, topk_weights, workspace, stream=None, handle=No
                               _ptr(topk_weights), _ptr(active_ranks), _ptr(workspace),
                               workspace.numel() * workspace.element_size(),
                               ctypes.byref(h), _stream(stream)), "moe_dispatch")
+    return h
+
+
+def moe_dispatch_fp8(g, x_codes, x_scales, topk_ids, topk_weights, workspace, stream=None, handle=None,
+                     active_ranks=None) -> MoeHandle:
+    """moe_dispatch (FP8 geometry) of rows that moe_add_rmsnorm has quantised: codes [T, H] and
+    float32 scales [T, H / 128]."""
+    h = MoeHandle() if handle is None else handle
+    _check(lib().moe_dispatch_fp8(ctypes.byref(g), _ptr(x_codes), _ptr(x_scales), _ptr(topk_ids), _ids_dtype(topk_ids),
+                                  _ptr(topk_weights), _ptr(active_ranks), _ptr(workspace),
+                                  workspace.numel() * workspace.element_size(), ctypes.byref(h), _stream(stream)),
+           "moe_dispatch_fp8")
     return h
 
 
@@ -366,6 +379,22 @@ class MoELayer1GPU:
             _require(active_ranks, "active_ranks", (torch.int32,), (self.geom.world,), self.device)
         moe_dispatch(self.geom, x, topk_ids, topk_weights, self.workspace, handle=self.handle,
                      active_ranks=active_ranks)
+        return self.handle
+
+    def dispatch_fp8(self, x_codes, x_scales, topk_ids, topk_weights, active_ranks=None):
+        """dispatch (quant="fp8") of rows quantised already, as moe_add_rmsnorm writes them:
+        codes [T, H] (float8_e4m3fn or uint8) and float32 scales [T, H / 128]."""
+        import torch
+        g = self.geom
+        if self.quant != "fp8":
+            raise ValueError("dispatch_fp8 needs a layer with quant=\"fp8\"")
+        _require(x_codes, "x_codes", (torch.float8_e4m3fn, torch.uint8), (g.num_tokens, g.hidden), self.device)
+        _require(x_scales, "x_scales", (torch.float32,), (g.num_tokens, g.hidden // 128), self.device)
+        self._check_routing(topk_ids, topk_weights)
+        if active_ranks is not None:
+            _require(active_ranks, "active_ranks", (torch.int32,), (g.world,), self.device)
+        moe_dispatch_fp8(g, x_codes, x_scales, topk_ids, topk_weights, self.workspace, handle=self.handle,
+                         active_ranks=active_ranks)
         return self.handle
 
     def expert_ffn(self):

@@ -79,43 +79,58 @@ def _typed(t, name, dtypes):
         raise TypeError("%s: dtype %s, expected %s" % (name, t.dtype, " or ".join(str(d) for d in dtypes)))
 
 
-def _packed(t, name, dtypes, shape):
-    """The address of a contiguous tensor of one of `dtypes` and of `shape`; None stays None."""
-    if t is None:
-        return None
+def _refuse(t, name, dtypes, shape, dev, layout):
+    """Raises for what _packed or _rows found wrong."""
     _typed(t, name, dtypes)
     if t.shape != shape:
         raise ValueError("%s: shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
-    return t.data_ptr()
+    if t.get_device() != dev:
+        raise ValueError("%s is on %s; expected device %d" % (name, t.device, dev))
+    raise ValueError("%s: strides %s; %s" % (name, t.stride(), layout))
 
 
-def _rows(t, name, dtypes, shape):
+# Small calls take as long as their checks do on the host, so what is right is found out first.
+
+def _packed(t, name, dtypes, shape, dev):
+    """The address of a contiguous tensor of one of `dtypes`, of `shape` and on device `dev`;
+    None stays None."""
+    if t is None:
+        return None
+    if isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape and t.is_contiguous() \
+            and t.get_device() == dev:
+        return t.data_ptr()
+    _refuse(t, name, dtypes, shape, dev, "must be contiguous")
+
+
+def _rows(t, name, dtypes, shape, dev):
     """(address, row stride) of a matrix with packed columns."""
     if t is None:
         return None, 0
-    _typed(t, name, dtypes)
-    if t.shape != shape:
-        raise ValueError("%s: shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-    row, col = t.stride()
-    if (col != 1 and shape[1] > 1) or (row < shape[1] and shape[0] > 1):
-        raise ValueError("%s: strides %s; rows may lie apart, but not overlap, and columns are packed"
-                         % (name, t.stride()))
-    return t.data_ptr(), row if shape[0] > 1 else 0
+    if isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape and t.get_device() == dev:
+        if t.is_contiguous():
+            return t.data_ptr(), 0
+        row, col = t.stride()
+        if (col == 1 or shape[1] <= 1) and (row >= shape[1] or shape[0] <= 1):
+            return t.data_ptr(), row if shape[0] > 1 else 0
+    _refuse(t, name, dtypes, shape, dev, "rows may lie apart, but not overlap, and columns are packed")
 
 
-def _launch(stream, tensors):
-    """The stream's handle, after a look that every tensor is on its device."""
-    s = torch.cuda.current_stream() if stream is None else stream
-    dev = s.device_index
-    for name, t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError("%s is on %s; expected cuda:%d" % (name, t.device, dev))
-    return s.cuda_stream
+def _stream(stream, dev):
+    """The handle of the stream given, or of the current one, of device `dev`."""
+    if dev < 0:
+        raise ValueError("the tensors are in host memory; expected a CUDA device")
+    if stream is None:
+        if torch.cuda.current_device() != dev:
+            raise ValueError("the tensors are on cuda:%d, and the current device is cuda:%d"
+                             % (dev, torch.cuda.current_device()))
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device_index != dev:
+        raise ValueError("the tensors are on cuda:%d, and the stream is on cuda:%d" % (dev, stream.device_index))
+    return stream.cuda_stream
 
 
 _BF16, _F32, _ROW = (torch.bfloat16,), (torch.float32,), (torch.bfloat16, torch.float32)
+_E4M3, _BYTE = (torch.float8_e4m3fn, torch.uint8), (torch.uint8,)
 
 
 def moe_add_rmsnorm(x, residual, weight, eps, sum_out=None, out=None, out_fp8=None, scales=None, rstd=None,
@@ -129,25 +144,21 @@ def moe_add_rmsnorm(x, residual, weight, eps, sum_out=None, out=None, out_fp8=No
     _typed(x, "x", _BF16)
     if x.dim() != 2:
         raise ValueError("x: shape %s, expected [tokens, hidden]" % (tuple(x.shape),))
-    shape = x.shape
-    T, H = shape
-    n = MoeNorm(T, H, 0, 0, eps)
-    px, n.x_stride = _rows(x, "x", _BF16, shape)
-    pr, n.residual_stride = _rows(residual, "residual", _ROW, shape)
-    ps, n.sum_stride = _rows(sum_out, "sum_out", _ROW if residual is None else (residual.dtype,), shape)
-    po, n.out_stride = _rows(out, "out", _BF16, shape)
-    pq = _packed(out_fp8, "out_fp8", (torch.float8_e4m3fn, torch.uint8), shape)
-    pc = _packed(scales, "scales", _F32, (T, H // 128))
-    pw = _packed(weight, "weight", _ROW, (H,))
-    pd = _packed(rstd, "rstd", _F32, (T,))
-    if pw is None or (out is None and out_fp8 is None) or (out_fp8 is None) != (scales is None):
+    if weight is None or (out is None and out_fp8 is None) or (out_fp8 is None) != (scales is None):
         raise ValueError("weight, and out or out_fp8 with scales, must be given")
-    stream_of = residual if residual is not None else sum_out
-    n.residual_dtype = 0 if stream_of is None else DTYPE[stream_of.dtype]
-    n.weight_dtype = DTYPE[weight.dtype]
-    s = _launch(stream, (("x", x), ("residual", residual), ("weight", weight), ("sum_out", sum_out), ("out", out),
-                         ("out_fp8", out_fp8), ("scales", scales), ("rstd", rstd)))
-    _call(_lib().moe_add_rmsnorm(n, px, pr, pw, ps, po, pq, pc, pd, s), "moe_add_rmsnorm")
+    shape, dev = x.shape, x.get_device()
+    T, H = shape
+    px, xs = _rows(x, "x", _BF16, shape, dev)
+    pr, rs = _rows(residual, "residual", _ROW, shape, dev)
+    ps, ss = _rows(sum_out, "sum_out", _ROW if residual is None else (residual.dtype,), shape, dev)
+    po, os = _rows(out, "out", _BF16, shape, dev)
+    pw = _packed(weight, "weight", _ROW, (H,), dev)
+    pq = _packed(out_fp8, "out_fp8", _E4M3, shape, dev)
+    pc = _packed(scales, "scales", _F32, (T, H // 128), dev)
+    pd = _packed(rstd, "rstd", _F32, (T,), dev)
+    h = sum_out if residual is None else residual
+    n = MoeNorm(T, H, 0 if h is None else DTYPE[h.dtype], DTYPE[weight.dtype], eps, xs, rs, ss, os)
+    _call(_lib().moe_add_rmsnorm(n, px, pr, pw, ps, po, pq, pc, pd, _stream(stream, dev)), "moe_add_rmsnorm")
 
 
 def moe_add_rmsnorm_workspace_size(tokens, hidden):
@@ -165,24 +176,22 @@ def moe_add_rmsnorm_backward(dout, h, weight, rstd, dx, dweight, workspace, dsum
     _typed(dout, "dout", _BF16)
     if dout.dim() != 2:
         raise ValueError("dout: shape %s, expected [tokens, hidden]" % (tuple(dout.shape),))
-    shape = dout.shape
-    T, H = shape
     _typed(h, "h", _ROW)
-    n = MoeNorm(T, H, DTYPE[h.dtype], 0, 0.0)
-    pg, n.x_stride = _rows(dout, "dout", _BF16, shape)
-    ph, n.residual_stride = _rows(h, "h", _ROW, shape)
-    ps, n.sum_stride = _rows(dsum, "dsum", (h.dtype,), shape)
-    px, n.out_stride = _rows(dx, "dx", (h.dtype,), shape)
-    pw = _packed(weight, "weight", _ROW, (H,))
-    pr = _packed(rstd, "rstd", _F32, (T,))
-    pd = _packed(dweight, "dweight", _F32, (H,))
-    _typed(workspace, "workspace", (torch.uint8,))
-    if None in (pw, pr, pd, px) or not workspace.is_contiguous():
-        raise ValueError("weight, rstd, dx, dweight and a contiguous workspace must be given")
-    n.weight_dtype = DTYPE[weight.dtype]
-    s = _launch(stream, (("dout", dout), ("h", h), ("weight", weight), ("rstd", rstd), ("dsum", dsum), ("dx", dx),
-                         ("dweight", dweight), ("workspace", workspace)))
-    _call(_lib().moe_add_rmsnorm_backward(n, pg, ph, pw, pr, ps, px, pd, workspace.data_ptr(), workspace.numel(), s),
+    _typed(workspace, "workspace", _BYTE)
+    shape, dev, same = dout.shape, dout.get_device(), (h.dtype,)
+    T, H = shape
+    pg, gs = _rows(dout, "dout", _BF16, shape, dev)
+    ph, hs = _rows(h, "h", same, shape, dev)
+    ps, ss = _rows(dsum, "dsum", same, shape, dev)
+    px, xs = _rows(dx, "dx", same, shape, dev)
+    pw = _packed(weight, "weight", _ROW, (H,), dev)
+    pr = _packed(rstd, "rstd", _F32, (T,), dev)
+    pd = _packed(dweight, "dweight", _F32, (H,), dev)
+    pk = _packed(workspace, "workspace", _BYTE, workspace.shape, dev)
+    if None in (pw, pr, pd, px):
+        raise ValueError("weight, rstd, dx and dweight must be given")
+    n = MoeNorm(T, H, DTYPE[h.dtype], DTYPE[weight.dtype], 0.0, gs, hs, ss, xs)
+    _call(_lib().moe_add_rmsnorm_backward(n, pg, ph, pw, pr, ps, px, pd, pk, workspace.numel(), _stream(stream, dev)),
           "moe_add_rmsnorm_backward")
 
 
@@ -196,39 +205,42 @@ def make_router(num_experts, top_k, score="softmax", groups=1, top_groups=None, 
 
 
 def _route(r, logits):
+    """The rule for these logits, their address, shape [T, k] of the picks and device."""
     _typed(logits, "logits", _ROW)
     if logits.dim() != 2 or logits.shape[1] != r.num_experts:
         raise ValueError("logits: shape %s, expected [tokens, %d]" % (tuple(logits.shape), r.num_experts))
-    p, stride = _rows(logits, "logits", _ROW, logits.shape)
-    rule = MoeRouter.from_buffer_copy(r)   # the caller's rule stays as it is
-    rule.logits_dtype, rule.logits_stride = DTYPE[logits.dtype], stride
-    return rule, p, logits.shape[0]
+    dev = logits.get_device()
+    p, stride = _rows(logits, "logits", _ROW, logits.shape, dev)
+    dtype = DTYPE[logits.dtype]
+    if r.logits_dtype != dtype or r.logits_stride != stride:
+        r = MoeRouter.from_buffer_copy(r)   # the caller's rule stays as it is
+        r.logits_dtype, r.logits_stride = dtype, stride
+    return r, p, (logits.shape[0], r.top_k), dev
 
 
 def moe_route_topk(r, logits, bias, topk_ids, topk_weights, stream=None):
     """Expert ids (int32 or int64 [T, k], -1 where no expert is left) and routing weights
     (float32 [T, k]) from the gate's logits (bf16 or float32 [T, E]) by the rule `r`
     (make_router).  bias: float32 [E], added to the scores for the picking alone, or None."""
-    rule, pl, T = _route(r, logits)
-    pb = _packed(bias, "bias", _F32, (r.num_experts,))
-    pi = _packed(topk_ids, "topk_ids", tuple(_IDS), (T, r.top_k))
-    pw = _packed(topk_weights, "topk_weights", _F32, (T, r.top_k))
+    r, pl, picks, dev = _route(r, logits)
+    pb = _packed(bias, "bias", _F32, (r.num_experts,), dev)
+    pi = _packed(topk_ids, "topk_ids", _IDS, picks, dev)
+    pw = _packed(topk_weights, "topk_weights", _F32, picks, dev)
     if pi is None or pw is None:
         raise ValueError("topk_ids and topk_weights must be given")
-    s = _launch(stream, (("logits", logits), ("bias", bias), ("topk_ids", topk_ids), ("topk_weights", topk_weights)))
-    _call(_lib().moe_route_topk(rule, T, pl, pb, pi, _IDS[topk_ids.dtype], pw, s), "moe_route_topk")
+    _call(_lib().moe_route_topk(r, picks[0], pl, pb, pi, _IDS[topk_ids.dtype], pw, _stream(stream, dev)),
+          "moe_route_topk")
 
 
 def moe_route_topk_backward(r, logits, topk_ids, dweights, dlogits, stream=None):
     """dlogits (contiguous, of the logits' type) from dweights, the picks held fixed."""
-    rule, pl, T = _route(r, logits)
-    pi = _packed(topk_ids, "topk_ids", tuple(_IDS), (T, r.top_k))
-    pw = _packed(dweights, "dweights", _F32, (T, r.top_k))
-    pd = _packed(dlogits, "dlogits", (logits.dtype,), logits.shape)
+    r, pl, picks, dev = _route(r, logits)
+    pi = _packed(topk_ids, "topk_ids", _IDS, picks, dev)
+    pw = _packed(dweights, "dweights", _F32, picks, dev)
+    pd = _packed(dlogits, "dlogits", (logits.dtype,), logits.shape, dev)
     if None in (pi, pw, pd):
         raise ValueError("topk_ids, dweights and dlogits must be given")
-    s = _launch(stream, (("logits", logits), ("topk_ids", topk_ids), ("dweights", dweights), ("dlogits", dlogits)))
-    _call(_lib().moe_route_topk_backward(rule, T, pl, pi, _IDS[topk_ids.dtype], pw, pd, s),
+    _call(_lib().moe_route_topk_backward(r, picks[0], pl, pi, _IDS[topk_ids.dtype], pw, pd, _stream(stream, dev)),
           "moe_route_topk_backward")
 
 
@@ -238,14 +250,14 @@ def moe_quantize_w4(w, group, codes, scales, stream=None):
     _typed(w, "w", _BF16)
     if w.dim() < 1 or group not in (32, 64, 128) or w.shape[-1] % group:
         raise ValueError("w: shape %s, expected whole groups of 32, 64 or 128 columns" % (tuple(w.shape),))
-    cols = w.shape[-1]
-    pw = _packed(w, "w", _BF16, w.shape)
-    pc = _packed(codes, "codes", (torch.uint8,), w.shape[:-1] + (cols // 2,))
-    ps = _packed(scales, "scales", _BF16, w.shape[:-1] + (cols // group,))
+    cols, dev = w.shape[-1], w.get_device()
+    pw = _packed(w, "w", _BF16, w.shape, dev)
+    pc = _packed(codes, "codes", _BYTE, w.shape[:-1] + (cols // 2,), dev)
+    ps = _packed(scales, "scales", _BF16, w.shape[:-1] + (cols // group,), dev)
     if pc is None or ps is None:
         raise ValueError("codes and scales must be given")
-    s = _launch(stream, (("w", w), ("codes", codes), ("scales", scales)))
-    _call(_lib().moe_quantize_w4(w.numel() // max(cols, 1), cols, group, pw, pc, ps, s), "moe_quantize_w4")
+    _call(_lib().moe_quantize_w4(w.numel() // max(cols, 1), cols, group, pw, pc, ps, _stream(stream, dev)),
+          "moe_quantize_w4")
 
 
 def make_w4_geom(tokens, hidden, experts, k, intermediate, group):
@@ -275,22 +287,24 @@ class MoELayerW4:
         self.status_word = torch.zeros(1, dtype=torch.int32, device=self.device)
         self.weights = None
         self._addresses = None
+        self._buffers = (self.out.data_ptr(), self.status_word.data_ptr(), self.workspace.data_ptr(),
+                         self.workspace.numel())
 
     def set_weights(self, w1, s1, w2, s2):
         """Codes w1 uint8 [E, 2I, H / 2] (gate rows, then up rows) and w2 [E, H, I / 2] with bf16
         scales s1 [E, 2I, H / group] and s2 [E, H, I / group]; put in the kernels' order once here."""
         g = self.geom
         E, H, I, G = g.num_experts, g.hidden, g.intermediate, g.group
-        given = [(w1, "w1", (torch.uint8,), (E, 2 * I, H // 2)), (s1, "s1", _BF16, (E, 2 * I, H // G)),
-                 (w2, "w2", (torch.uint8,), (E, H, I // 2)), (s2, "s2", _BF16, (E, H, I // G))]
-        for t, name, dtypes, shape in given:
-            if _packed(t, name, dtypes, shape) is None:
-                raise ValueError("%s must be given" % name)
-        s = _launch(None, [(name, t) for t, name, _, _ in given])
+        given = [(w1, "w1", _BYTE, (E, 2 * I, H // 2)), (s1, "s1", _BF16, (E, 2 * I, H // G)),
+                 (w2, "w2", _BYTE, (E, H, I // 2)), (s2, "s2", _BF16, (E, H, I // G))]
+        dev = self.out.get_device()
+        natural = [_packed(*one, dev) for one in given]
+        if None in natural:
+            raise ValueError("w1, s1, w2 and s2 must be given")
+        s = _stream(None, dev)
         self.weights = [torch.empty_like(t) for t, _, _, _ in given]
         self._addresses = [t.data_ptr() for t in self.weights]
-        _call(_lib().moe_prepare_weights_w4(g, *(t.data_ptr() for t, _, _, _ in given), *self._addresses, s),
-              "moe_prepare_weights_w4")
+        _call(_lib().moe_prepare_weights_w4(g, *natural, *self._addresses, s), "moe_prepare_weights_w4")
 
     def quantize_weights(self, w1, w2):
         """set_weights from bf16 w1 [E, 2I, H] and w2 [E, H, I]."""
@@ -298,7 +312,7 @@ class MoELayerW4:
         E, H, I, G = g.num_experts, g.hidden, g.intermediate, g.group
         given = []
         for w, name, shape in ((w1, "w1", (E, 2 * I, H)), (w2, "w2", (E, H, I))):
-            if _packed(w, name, _BF16, shape) is None:
+            if _packed(w, name, _BF16, shape, self.out.get_device()) is None:
                 raise ValueError("%s must be given" % name)
             codes = torch.empty(shape[:2] + (shape[2] // 2,), dtype=torch.uint8, device=w.device)
             scales = torch.empty(shape[:2] + (shape[2] // G,), dtype=torch.bfloat16, device=w.device)
@@ -311,19 +325,18 @@ class MoELayerW4:
             raise RuntimeError("set_weights() has not been called")
         g = self.geom
         _typed(x, "x", _BF16)
-        T = x.shape[0] if x.dim() else 0
+        T, dev = x.shape[0] if x.dim() else 0, self.out.get_device()
         if T > self.max_tokens:
             raise ValueError("x: %d tokens, at most %d" % (T, self.max_tokens))
-        px = _packed(x, "x", _BF16, (T, g.hidden))
-        pi = _packed(topk_ids, "topk_ids", tuple(_IDS), (T, g.top_k))
-        pw = _packed(topk_weights, "topk_weights", _F32, (T, g.top_k))
+        px = _packed(x, "x", _BF16, (T, g.hidden), dev)
+        pi = _packed(topk_ids, "topk_ids", _IDS, (T, g.top_k), dev)
+        pw = _packed(topk_weights, "topk_weights", _F32, (T, g.top_k), dev)
         if pi is None or pw is None:
             raise ValueError("topk_ids and topk_weights must be given")
-        s = _launch(stream, (("x", x), ("topk_ids", topk_ids), ("topk_weights", topk_weights), ("the layer", self.out)))
-        call = g if T == self.max_tokens else make_w4_geom(T, g.hidden, g.num_experts, g.top_k, g.intermediate, g.group)
-        _call(_lib().moe_forward_w4(call, px, pi, _IDS[topk_ids.dtype], pw, *self._addresses, self.out.data_ptr(),
-                                    self.status_word.data_ptr(), self.workspace.data_ptr(), self.workspace.numel(), s),
-              "moe_forward_w4")
+        if T != self.max_tokens:
+            g = make_w4_geom(T, g.hidden, g.num_experts, g.top_k, g.intermediate, g.group)
+        _call(_lib().moe_forward_w4(g, px, pi, _IDS[topk_ids.dtype], pw, *self._addresses, *self._buffers,
+                                    _stream(stream, dev)), "moe_forward_w4")
         return self.out if T == self.max_tokens else self.out[:T]
 
     def status(self):

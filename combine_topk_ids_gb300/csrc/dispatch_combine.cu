@@ -505,9 +505,12 @@ __device__ __forceinline__ uint32_t e4m3x4(float v0, float v1, float v2, float v
 // FP8 dispatch: like dispatch_copy_kernel, but each 128-column block of x[t] is quantised
 // once (16 lanes x 8 columns: the half-warp reduces amax) and the e4m3 codes plus the
 // block scale are written to every receive row of the token (and for RM/FLAT to its
-// pick-ordered rows).
+// pick-ordered rows).  CODES: x comes as codes and scales already (half the bytes to read)
+// and is copied as it is.
 struct QuantCopyArgs {
     const uint16_t *x;
+    const uint8_t *xq;      // CODES: [T, H] codes
+    const float *xs;        // CODES: [T, H/128]
     uint8_t *recv;          // [nrecv, H] codes
     float *recv_scales;     // [H/128][nrecv]
     uint8_t *apick;         // RM/FLAT: [P, H] codes in pick-list order
@@ -517,6 +520,7 @@ struct QuantCopyArgs {
     int64_t cap, nrecv, P;
 };
 
+template <bool CODES>
 __global__ void __launch_bounds__(kCopyThreads) dispatch_quant_kernel(QuantCopyArgs a) {
     pdl_begin();   // after the previous kernel in the stream (programmatic launch)
     __shared__ int64_t dst[kWarpsPerBlock][kMaxDst];   // row index of each target row
@@ -547,6 +551,11 @@ __global__ void __launch_bounds__(kCopyThreads) dispatch_quant_kernel(QuantCopyA
 #pragma unroll
     for (int u = 0; u < kCopyU; ++u) {
         const int c = c0 + 32 * u;
+        if (CODES) {
+            q[u] = c < nv ? reinterpret_cast<const uint2 *>(a.xq + t * a.H)[c] : make_uint2(0, 0);
+            sc[u] = c < nv ? a.xs[t * (a.H / 128) + (c >> 4)] : 0.f;
+            continue;
+        }
         // c < nv is the same for the 16 lanes of a block (H is a multiple of 128)
         const uint4 v = c < nv ? ld_nc_v4(src + c) : make_uint4(0, 0, 0, 0);
         float f[8] = {bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y),
@@ -724,14 +733,24 @@ cudaError_t launch_prepare_w1(const moe_geom &g, const uint16_t *w1, uint16_t *w
     return cudaGetLastError();
 }
 
-cudaError_t launch_dispatch_quant(const Routing &r, const uint16_t *x, cudaStream_t s) {
+static cudaError_t dispatch_quant(const Routing &r, const uint16_t *x, const uint8_t *xq, const float *xs,
+                                  cudaStream_t s) {
     const Plan &p = *r.p;
     if (p.T == 0) return cudaSuccess;
     const int nchunk = (int)((p.H / 8 + 32 * kCopyU - 1) / (32 * kCopyU));
-    QuantCopyArgs a{x, reinterpret_cast<uint8_t *>(r.recv_x), r.recv_scales, reinterpret_cast<uint8_t *>(r.apick),
+    QuantCopyArgs a{x, xq, xs, reinterpret_cast<uint8_t *>(r.recv_x), r.recv_scales, reinterpret_cast<uint8_t *>(r.apick),
                     r.apick_scales, r.slot, r.recv_row, r.pick_pos, (int)p.T, (int)p.k, (int)p.W, (int)p.H,
                     p.layout, nchunk, p.cap, p.nrecv, p.P};
-    return launch_pdl(dispatch_quant_kernel, dim3(blocks_for(p.T * nchunk)), dim3(kCopyThreads), 0, s, a);
+    return launch_pdl(xq ? dispatch_quant_kernel<true> : dispatch_quant_kernel<false>, dim3(blocks_for(p.T * nchunk)),
+                      dim3(kCopyThreads), 0, s, a);
+}
+
+cudaError_t launch_dispatch_quant(const Routing &r, const uint16_t *x, cudaStream_t s) {
+    return dispatch_quant(r, x, nullptr, nullptr, s);
+}
+
+cudaError_t launch_dispatch_codes(const Routing &r, const uint8_t *xq, const float *xs, cudaStream_t s) {
+    return dispatch_quant(r, nullptr, xq, xs, s);
 }
 
 cudaError_t launch_quantize_weights_fp8(const uint16_t *w, int64_t E, int64_t rows, int64_t cols,

@@ -4,6 +4,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "../../include/moe_block.h"
 #include "moe_internal.cuh"
 
 namespace moe {
@@ -212,9 +213,10 @@ int moe_expert_out_size(const moe_geom *g, size_t *bytes) {
     return MOE_OK;
 }
 
-int moe_dispatch(const moe_geom *g, const void *x_dev, const void *topk_ids_dev, int ids_dtype,
-                 const float *topk_weights_dev, const int32_t *active_ranks_dev, void *workspace_dev,
-                 size_t workspace_bytes, moe_handle *h, void *stream) {
+// moe_dispatch, and with x_scales_dev moe_dispatch_fp8 (x_dev then holds codes).
+static int dispatch(const moe_geom *g, const void *x_dev, const float *x_scales_dev, const void *topk_ids_dev,
+                    int ids_dtype, const float *topk_weights_dev, const int32_t *active_ranks_dev,
+                    void *workspace_dev, size_t workspace_bytes, moe_handle *h, void *stream) {
     if (!g || !h || !workspace_dev) return MOE_ERR_INVALID_ARGUMENT;
     if (ids_dtype != MOE_IDS_INT32 && ids_dtype != MOE_IDS_INT64) return MOE_ERR_IDS_DTYPE;
     Plan p;
@@ -269,13 +271,32 @@ int moe_dispatch(const moe_geom *g, const void *x_dev, const void *topk_ids_dev,
                        active_ranks_dev, s) != cudaSuccess)
         return MOE_ERR_CUDA;
     record(h, MOE_EV_ROUTING_END, s);
-    const cudaError_t ce = p.quant == MOE_QUANT_FP8_E4M3
+    const cudaError_t ce = x_scales_dev ? launch_dispatch_codes(r, static_cast<const uint8_t *>(x_dev), x_scales_dev, s)
+                           : p.quant == MOE_QUANT_FP8_E4M3
                                ? launch_dispatch_quant(r, static_cast<const uint16_t *>(x_dev), s)
                                : launch_dispatch_copy(r, static_cast<const uint16_t *>(x_dev), s);
     if (ce != cudaSuccess) return MOE_ERR_CUDA;
     record(h, MOE_EV_DISPATCH_END, s);
     h->magic = kHandleMagic;
     return MOE_OK;
+}
+
+int moe_dispatch(const moe_geom *g, const void *x_dev, const void *topk_ids_dev, int ids_dtype,
+                 const float *topk_weights_dev, const int32_t *active_ranks_dev, void *workspace_dev,
+                 size_t workspace_bytes, moe_handle *h, void *stream) {
+    return dispatch(g, x_dev, nullptr, topk_ids_dev, ids_dtype, topk_weights_dev, active_ranks_dev, workspace_dev,
+                    workspace_bytes, h, stream);
+}
+
+int moe_dispatch_fp8(const moe_geom *g, const uint8_t *x_codes_dev, const float *x_scales_dev,
+                     const void *topk_ids_dev, int ids_dtype, const float *topk_weights_dev,
+                     const int32_t *active_ranks_dev, void *workspace_dev, size_t workspace_bytes, moe_handle *h,
+                     void *stream) {
+    if (!g || g->quant != MOE_QUANT_FP8_E4M3) return MOE_ERR_INVALID_ARGUMENT;
+    if (g->num_tokens > 0 && !x_scales_dev) return MOE_ERR_INVALID_ARGUMENT;
+    if (!aligned(x_scales_dev, 4)) return MOE_ERR_MISALIGNED;
+    return dispatch(g, x_codes_dev, x_scales_dev, topk_ids_dev, ids_dtype, topk_weights_dev, active_ranks_dev,
+                    workspace_dev, workspace_bytes, h, stream);
 }
 
 int moe_prepare_weights(const moe_geom *g, const void *w1_dev, void *w1_prepared_dev, void *stream) {

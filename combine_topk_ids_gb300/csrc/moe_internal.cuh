@@ -84,6 +84,8 @@ int launch_gemm2(const Routing &r, const uint16_t *w2, void *expert_out, cudaStr
 
 // ---- FP8 (moe_quant MOE_QUANT_FP8_E4M3) -----------------------------------------------
 cudaError_t launch_dispatch_quant(const Routing &r, const uint16_t *x, cudaStream_t s);
+// x as e4m3 codes [T, H] and scales [T, H/128]
+cudaError_t launch_dispatch_codes(const Routing &r, const uint8_t *xq, const float *xs, cudaStream_t s);
 // 128x128-block quantisation of bf16 [E, rows, cols] weights; w1_inter = I interleaves the
 // gate/up row blocks of W1 (0: keep the order)
 cudaError_t launch_quantize_weights_fp8(const uint16_t *w, int64_t E, int64_t rows, int64_t cols,

@@ -75,6 +75,18 @@ int moe_add_rmsnorm_backward(const moe_norm *n, const void *dout_dev, const void
                              const float *rstd_dev, const void *dsum_dev, void *dx_dev, float *dweight_dev,
                              void *workspace_dev, size_t workspace_bytes, void *stream);
 
+/*
+ * moe_dispatch_fp8 - moe_dispatch for an FP8 geometry (MOE_QUANT_FP8_E4M3) and rows that are
+ *   quantised already: x_codes_dev [num_tokens, hidden] and x_scales_dev [num_tokens,
+ *   hidden / 128], as moe_add_rmsnorm writes them.  They are copied as they are; everything
+ *   else, the handle among it, is as after moe_dispatch.
+ *   Errors: those of moe_dispatch, and MOE_ERR_INVALID_ARGUMENT for a bf16 geometry or NULL scales.
+ */
+int moe_dispatch_fp8(const moe_geom *g, const uint8_t *x_codes_dev, const float *x_scales_dev,
+                     const void *topk_ids_dev, int ids_dtype, const float *topk_weights_dev,
+                     const int32_t *active_ranks_dev, void *workspace_dev, size_t workspace_bytes,
+                     moe_handle *handle, void *stream);
+
 /* ---- router ----------------------------------------------------------------------------- */
 
 typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
