@@ -1,0 +1,216 @@
+// The gradient of the residual addition and RMS norm (moe_add_rmsnorm_backward; declared in
+// include/moe_block.h).
+//
+// With g = dout * w and xhat = h * rstd, one row:
+//     dx = rstd * (g - xhat * mean(g * xhat)) + dsum;     dw += dout * xhat
+// dout, h and dsum are read once, dx is written once; the columns' sums stay in registers over a
+// block's rows and are added up by a second kernel in a fixed order.  HBM bounds it.
+#include "norm.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kMaxParts = 304;   // row blocks that write a partial dweight (two per SM)
+
+struct NormBackArgs {
+    const void *dout, *h, *w, *dsum;
+    void *dx;
+    const float *rstd;
+    float *part;              // [gridDim.x][H]
+    int64_t ds, hs, ss, os;   // row strides in elements
+    int T, H;
+};
+
+// Each block takes every gridDim.x-th group of blockDim.y rows and keeps its columns' sums of
+// dout * xhat in registers; they leave as one row of `part`.  A row's inputs are under way
+// while the row before it is computed.  ODD: rows off 16-byte boundaries.
+template <int VPT, int MAXT, bool R32, bool W32, bool ODD>
+__global__ void __launch_bounds__(MAXT) add_rmsnorm_backward_kernel(NormBackArgs a) {
+    __shared__ float red[2][32];
+    extern __shared__ float cols[];   // [H] when blockDim.y > 1
+    pdl_begin();
+    float dw[VPT][8];
+#pragma unroll
+    for (int v = 0; v < VPT; ++v)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dw[v][j] = 0.f;
+    Raw8<W32, ODD> rw[VPT];
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) rw[v].load(a.w, 8 * (int)(threadIdx.x + v * blockDim.x), a.H);
+    Raw8<false, ODD, ODD> rg[VPT];
+    Raw8<R32, ODD, ODD> rh[VPT], rs[VPT];
+    auto dout = [&](int64_t t) { return static_cast<const __nv_bfloat16 *>(a.dout) + (t < a.T ? t : 0) * a.ds; };
+    auto h = [&](int64_t t) { return static_cast<const char *>(a.h) + (t < a.T ? t : 0) * a.hs * (R32 ? 4 : 2); };
+    auto dsum = [&](int64_t t) { return static_cast<const char *>(a.dsum) + (t < a.T ? t : 0) * a.ss * (R32 ? 4 : 2); };
+    auto columns = [&](int64_t t) { return t < a.T ? a.H : 0; };   // rows past the end have none
+    auto fetch = [&](int64_t t) {
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            const int i = 8 * (int)(threadIdx.x + v * blockDim.x);
+            rg[v].load(dout(t), i, columns(t));
+            rh[v].load(h(t), i, columns(t));
+        }
+    };
+    auto fetch_dsum = [&](int64_t t) {
+        if (a.dsum)
+#pragma unroll
+            for (int v = 0; v < VPT; ++v) rs[v].load(dsum(t), 8 * (int)(threadIdx.x + v * blockDim.x), columns(t));
+    };
+    const int64_t groups = ((int64_t)a.T + blockDim.y - 1) / blockDim.y, step = (int64_t)gridDim.x * blockDim.y;
+    int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    fetch(t);
+    fetch_dsum(t);
+    float rstd = t < a.T ? a.rstd[t] : 0.f;
+    int turn = 0;
+    for (int64_t gr = blockIdx.x; gr < groups; gr += gridDim.x, t += step) {
+        const float rt = rstd;
+        float g[VPT][8], xh[VPT][8];
+        float along = 0.f;
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            const int i = 8 * (int)(threadIdx.x + v * blockDim.x);
+            float w[8];
+            rg[v].floats(dout(t), i, columns(t), g[v]);
+            rh[v].floats(h(t), i, columns(t), xh[v]);
+            rw[v].floats(a.w, i, columns(t), w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                xh[v][j] *= rt;
+                dw[v][j] = fmaf(g[v][j], xh[v][j], dw[v][j]);
+                g[v][j] *= w[j];
+                along = fmaf(g[v][j], xh[v][j], along);
+            }
+        }
+        fetch(t + step);
+        rstd = t + step < a.T ? a.rstd[t + step] : 0.f;
+        along = row_sum(along, red[turn]) / (float)a.H;   // (two turns: the last row's sums are read until the next barrier)
+        turn ^= 1;
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            const int i = 8 * (int)(threadIdx.x + v * blockDim.x);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) g[v][j] = rt * (g[v][j] - xh[v][j] * along);
+            if (a.dsum) {
+                float d[8];
+                rs[v].floats(dsum(t), i, columns(t), d);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) g[v][j] += d[j];
+            }
+        }
+        // (dx may be dsum: this row's is read by now, and the next row is another)
+        fetch_dsum(t + step);
+#pragma unroll
+        for (int v = 0; v < VPT; ++v)
+            store8<R32, ODD>(static_cast<char *>(a.dx) + (t < a.T ? t : 0) * a.os * (R32 ? 4 : 2),
+                        8 * (int)(threadIdx.x + v * blockDim.x), columns(t), g[v]);
+    }
+    __syncthreads();
+    float *part = a.part + (int64_t)blockIdx.x * a.H;
+    if (blockDim.y == 1) {
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) store8<true, ODD>(part, 8 * (int)(threadIdx.x + v * blockDim.x), a.H, dw[v]);
+        return;
+    }
+    for (int y = 0; y < (int)blockDim.y; ++y) {   // the rows' sums in a fixed order
+        if ((int)threadIdx.y == y) {
+#pragma unroll
+            for (int v = 0; v < VPT; ++v)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int i = 8 * (int)(threadIdx.x + v * blockDim.x) + j;
+                    if (i < a.H) cols[i] = (y ? cols[i] : 0.f) + dw[v][j];
+                }
+        }
+        __syncthreads();
+    }
+    for (int i = threadIdx.y * blockDim.x + threadIdx.x; i < a.H; i += blockDim.x * blockDim.y) part[i] = cols[i];
+}
+
+// dweight = sum of the partial rows: 32 columns per block, row r of `part` on thread row r % 32.
+__global__ void __launch_bounds__(1024) sum_parts_kernel(const float *part, float *dw, int parts, int H) {
+    __shared__ float tile[32][33];
+    pdl_begin();
+    const int c = blockIdx.x * 32 + threadIdx.x;
+    float v = 0.f;
+    if (c < H)
+        for (int r = threadIdx.y; r < parts; r += 32) v += part[(int64_t)r * H + c];
+    tile[threadIdx.y][threadIdx.x] = v;
+    __syncthreads();
+    if (threadIdx.y != 0 || c >= H) return;
+    v = 0.f;
+    for (int r = 0; r < 32; ++r) v += tile[r][threadIdx.x];
+    dw[c] = v;
+}
+
+// The gradient holds more for each column (the column's sum, a second input): 2 chunks per
+// thread up to 8192 columns, 4 up to 16384, 8 above.
+NormShape norm_back_shape(int64_t chunks) { return spread(chunks, chunks <= 1024 ? 2 : chunks <= 2048 ? 4 : 8); }
+
+int backward_blocks(const moe_norm *n, const NormShape &sh) {
+    const int64_t groups = ((int64_t)n->num_tokens + sh.rows - 1) / sh.rows;
+    return (int)(groups < kMaxParts ? groups : kMaxParts);
+}
+
+template <typename F>
+cudaError_t with_shape(const NormShape &sh, bool r32, bool w32, bool odd, F &&f) {
+    if (sh.vpt == 2) return with_types(Shape<2, 512>{}, r32, w32, odd, f);
+    if (sh.vpt == 4) return with_types(Shape<4, 512>{}, r32, w32, odd, f);
+    return with_types(Shape<8, 1024>{}, r32, w32, odd, f);
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+int moe_add_rmsnorm_workspace_size(const moe_norm *n, size_t *bytes) {
+    int rc = check_norm(n);
+    if (rc != MOE_OK) return rc;
+    if (!bytes) return MOE_ERR_INVALID_ARGUMENT;
+    *bytes = (size_t)kMaxParts * (size_t)n->hidden * 4;
+    return MOE_OK;
+}
+
+int moe_add_rmsnorm_backward(const moe_norm *n, const void *dout_dev, const void *h_dev, const void *weight_dev,
+                             const float *rstd_dev, const void *dsum_dev, void *dx_dev, float *dweight_dev,
+                             void *workspace_dev, size_t workspace_bytes, void *stream) {
+    size_t need = 0;
+    int rc = moe_add_rmsnorm_workspace_size(n, &need);
+    if (rc != MOE_OK) return rc;
+    if (!dweight_dev || !workspace_dev ||
+        (n->num_tokens > 0 && (!dout_dev || !h_dev || !weight_dev || !rstd_dev || !dx_dev)))
+        return MOE_ERR_INVALID_ARGUMENT;
+    const size_t rb = dtype_bytes(n->residual_dtype);
+    if (!is_aligned(dout_dev, 2) || !is_aligned(h_dev, rb) || !is_aligned(weight_dev, dtype_bytes(n->weight_dtype)) ||
+        !is_aligned(rstd_dev, 4) || !is_aligned(dsum_dev, rb) || !is_aligned(dx_dev, rb) ||
+        !is_aligned(dweight_dev, 4) || !is_aligned(workspace_dev, 256))
+        return MOE_ERR_MISALIGNED;
+    if (workspace_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    if ((rc = check_device()) != MOE_OK) return rc;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const NormShape sh = norm_back_shape(((int64_t)n->hidden + 7) / 8);
+    const int blocks = backward_blocks(n, sh);
+    float *part = static_cast<float *>(workspace_dev);
+    if (blocks > 0) {
+        NormBackArgs a{dout_dev, h_dev, weight_dev, dsum_dev, dx_dev, rstd_dev, part, stride_of(n, n->x_stride),
+                       stride_of(n, n->residual_stride), stride_of(n, n->sum_stride),
+                       stride_of(n, n->out_stride), n->num_tokens, n->hidden};
+        const size_t smem = sh.rows > 1 ? (size_t)n->hidden * 4 : 0;   // at most 8 KB: rows > 1 below 2048 columns
+        const bool odd = n->hidden % 8 || !is_aligned(weight_dev, 16) || !even_rows(dout_dev, a.ds, 2) ||
+                         !even_rows(h_dev, a.hs, rb) || !even_rows(dsum_dev, a.ss, rb) || !even_rows(dx_dev, a.os, rb);
+        const cudaError_t e = with_shape(
+            sh, n->residual_dtype == MOE_DTYPE_FP32, n->weight_dtype == MOE_DTYPE_FP32, odd,
+            [&](auto v, auto r32, auto w32, auto odd) {
+                return launch_pdl(add_rmsnorm_backward_kernel<decltype(v)::vpt, decltype(v)::maxt, decltype(r32)::value,
+                                                              decltype(w32)::value, decltype(odd)::value>,
+                                  dim3(blocks), dim3(sh.threads, sh.rows), smem, s, a);
+            });
+        if (e != cudaSuccess) return MOE_ERR_CUDA;
+    }
+    return status_of(launch_pdl(sum_parts_kernel, dim3((n->hidden + 31) / 32), dim3(32, 32), 0, s,
+                                (const float *)part, dweight_dev, blocks, (int)n->hidden));
+}
+
+}  // extern "C"
