@@ -50,7 +50,7 @@ __device__ __forceinline__ uint2 quant8(const float (&y)[8], float &scale) {
 // 16 bytes at a time, the row's ends apart.  (A block then takes one group: what the next row's
 // inputs would hold of registers gives more blocks instead.)
 template <int VPT, int MAXT, bool R32, bool W32, bool ODD>
-__global__ void __launch_bounds__(MAXT, MAXT > 256 ? 1 : 8 / VPT < 3 ? 8 / VPT : ODD ? 4 : 2) add_rmsnorm_kernel(NormArgs a) {
+__global__ void __launch_bounds__(MAXT, MAXT > 256 ? 1 : 8 / VPT < 3 ? 8 / VPT : ODD ? 5 : 2) add_rmsnorm_kernel(NormArgs a) {
     __shared__ float red[2][32];
     pdl_begin();
     const int64_t groups = ((int64_t)a.T + blockDim.y - 1) / blockDim.y, step = (int64_t)gridDim.x * blockDim.y;
@@ -119,6 +119,7 @@ __global__ void __launch_bounds__(MAXT, MAXT > 256 ? 1 : 8 / VPT < 3 ? 8 / VPT :
                 }
             }
         }
+        if (ODD) break;
     }
 }
 
