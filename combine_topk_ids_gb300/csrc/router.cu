@@ -3,8 +3,7 @@
 // include/moe_block.h.
 //
 // One warp per token; lane l holds the EPL consecutive experts from l * EPL on, so that the
-// lowest lane with a value holds its lowest expert.  Keys are compared as 32-bit integers
-// whose order is that of the floats; 0 is "absent".
+// lowest lane with a value holds its lowest expert.  An absent expert's key is -infinity.
 //
 // The logits are read once and little is written, but a token's selection takes a few hundred
 // instructions for E = 256: the instruction issue bounds large batches, the launch small ones.
@@ -30,35 +29,32 @@ struct RouterArgs {
     float scale;
 };
 
-// Order-preserving image of a float; 0 for -infinity and NaN ("absent").  -0 counts as +0.
-__device__ __forceinline__ uint32_t key_of(float v) {
-    const uint32_t u = __float_as_uint(v + 0.0f);
-    const uint32_t o = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-    return v > -__int_as_float(0x7f800000) ? o : 0u;
-}
-__device__ __forceinline__ float of_key(uint32_t o) {
-    return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
+constexpr float kNone = -__builtin_huge_valf();   // the key of an absent expert
+constexpr float kMost = 3.402823466e38f;
+
+__device__ __forceinline__ float redux_max(float v) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
 }
 
-// A lane's logits as float32: -infinity beyond the last expert and for NaN; +infinity counts as
-// the largest finite value.  VEC: 16-byte (8-byte) loads; the lanes' experts then all exist or
-// none of them does.
+// A lane's EPL values of a row, `fill` beyond the last one.  VEC: four at a time; the lanes'
+// experts then all exist or none of them does.
 template <int EPL, bool VEC>
-__device__ __forceinline__ void load_logits(const RouterArgs &a, int64_t t, int first, float (&l)[EPL]) {
-    const float none = -__int_as_float(0x7f800000);
+__device__ __forceinline__ void load_values(const void *row, bool f32, int first, int E, float fill, float (&l)[EPL]) {
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) l[j] = none;
+    for (int j = 0; j < EPL; ++j) l[j] = fill;
     if (VEC) {
-        if (first < a.E) {
-            if (a.f32) {
-                const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(a.logits) + t * a.stride + first);
+        if (first < E) {
+            if (f32) {
+                const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(row) + first);
 #pragma unroll
                 for (int j = 0; j + 4 <= EPL; j += 4) {
                     const float4 v = p[j / 4];
                     l[j] = v.x; l[j + 1] = v.y; l[j + 2] = v.z; l[j + 3] = v.w;
                 }
             } else {
-                const uint2 *p = reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(a.logits) + t * a.stride + first);
+                const uint2 *p = reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(row) + first);
 #pragma unroll
                 for (int j = 0; j + 4 <= EPL; j += 4) {
                     const uint2 v = p[j / 4];
@@ -69,12 +65,21 @@ __device__ __forceinline__ void load_logits(const RouterArgs &a, int64_t t, int 
     } else {
 #pragma unroll
         for (int j = 0; j < EPL; ++j)
-            if (first + j < a.E)
-                l[j] = a.f32 ? static_cast<const float *>(a.logits)[t * a.stride + first + j]
-                             : __bfloat162float(static_cast<const __nv_bfloat16 *>(a.logits)[t * a.stride + first + j]);
+            if (first + j < E)
+                l[j] = f32 ? static_cast<const float *>(row)[first + j]
+                           : __bfloat162float(static_cast<const __nv_bfloat16 *>(row)[first + j]);
     }
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) l[j] = l[j] != l[j] ? none : fminf(l[j], 3.402823466e38f);
+}
+
+// -infinity for NaN; +infinity counts as the largest finite value.
+__device__ __forceinline__ float clean(float v) { return fmaxf(fminf(v != v ? kNone : v, kMost), kNone); }
+
+__device__ __forceinline__ const void *logits_row(const RouterArgs &a, int64_t t) {
+    return static_cast<const char *>(a.logits) + t * a.stride * (a.f32 ? 4 : 2);
+}
+__device__ __forceinline__ float logit(const RouterArgs &a, int64_t t, int e) {
+    const void *row = logits_row(a, t);
+    return clean(a.f32 ? static_cast<const float *>(row)[e] : __bfloat162float(static_cast<const __nv_bfloat16 *>(row)[e]));
 }
 
 // 1 / (1 + e^-v), the reciprocal to within 1 ulp.
@@ -87,7 +92,7 @@ __device__ __forceinline__ float warp_max(float v) {
 }
 template <int EPL>
 __device__ __forceinline__ float row_max(const float (&l)[EPL]) {
-    float m = -3.402823466e38f;   // the lowest finite value is a logit like any other
+    float m = -kMost;   // the lowest finite value is a logit like any other
 #pragma unroll
     for (int j = 0; j < EPL; ++j) m = fmaxf(m, l[j]);
     return warp_max(m);
@@ -114,57 +119,57 @@ __device__ __forceinline__ void score_row(const RouterArgs &a, const float (&l)[
     for (int j = 0; j < EPL; ++j) s[j] *= z;
 }
 
-// Takes the keys of experts outside the top_groups best groups out (0).
+// v joins a group's two largest keys.
+__device__ __forceinline__ void join(float v, float &first, float &second) {
+    second = fmaxf(second, fminf(first, v));
+    first = fmaxf(first, v);
+}
+
+// Takes the keys of experts outside the top_groups best groups out.
 template <int EPL>
-__device__ __forceinline__ void keep_groups(const RouterArgs &a, int lane, uint32_t (&key)[EPL], uint32_t *keys) {
-    const int size = a.E / a.groups;
-    uint32_t first = 0, second = 0;   // the group's two largest keys
+__device__ __forceinline__ void keep_groups(const RouterArgs &a, int lane, float (&key)[EPL], float *keys) {
+    float first = kNone, second = kNone;
     if (a.lanes_per_group > 0) {      // whole lanes, a power of two of them: exchanges among these
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) {
-            second = max(second, min(first, key[j]));
-            first = max(first, key[j]);
-        }
+        for (int j = 0; j < EPL; ++j) join(key[j], first, second);
         for (int o = 1; o < a.lanes_per_group; o <<= 1) {
-            const uint32_t f = __shfl_xor_sync(kAllLanes, first, o), s = __shfl_xor_sync(kAllLanes, second, o);
-            second = max(max(second, s), min(first, f));
-            first = max(first, f);
+            const float f = __shfl_xor_sync(kAllLanes, first, o), s = __shfl_xor_sync(kAllLanes, second, o);
+            second = fmaxf(fmaxf(second, s), fminf(first, f));
+            first = fmaxf(first, f);
         }
-        const uint32_t score = a.pair && second != 0 ? key_of(__fadd_rn(of_key(first), of_key(second))) : first;
+        const float score = a.pair && second > kNone ? first + second : first;
         const int mine = lane / a.lanes_per_group;
         int rank = 0;
+#pragma unroll 4
         for (int g = 0; g < a.groups; ++g) {
-            const uint32_t other = __shfl_sync(kAllLanes, score, g * a.lanes_per_group);
+            const float other = __shfl_sync(kAllLanes, score, g * a.lanes_per_group);
             rank += other > score || (other == score && g < mine);
         }
         if (rank >= a.top_groups)
 #pragma unroll
-            for (int j = 0; j < EPL; ++j) key[j] = 0;
+            for (int j = 0; j < EPL; ++j) key[j] = kNone;
         return;
     }
     // any other size: through shared memory, a lane to each group
+    const int size = a.E / a.groups;
 #pragma unroll
     for (int j = 0; j < EPL; ++j)
         if (lane * EPL + j < a.E) keys[lane * EPL + j] = key[j];
     __syncwarp();
     if (lane < a.groups)
-        for (int i = 0; i < size; ++i) {
-            const uint32_t v = keys[lane * size + i];
-            second = max(second, min(first, v));
-            first = max(first, v);
-        }
+        for (int i = 0; i < size; ++i) join(keys[lane * size + i], first, second);
     __syncwarp();
-    const uint32_t score = a.pair && second != 0 ? key_of(__fadd_rn(of_key(first), of_key(second))) : first;
+    const float score = a.pair && second > kNone ? first + second : first;
     int rank = 0;
     for (int g = 0; g < a.groups; ++g) {
-        const uint32_t other = __shfl_sync(kAllLanes, score, g);
+        const float other = __shfl_sync(kAllLanes, score, g);
         rank += other > score || (other == score && g < lane);
     }
     const uint32_t kept = __ballot_sync(kAllLanes, lane < a.groups && rank < a.top_groups);
     int g = lane * EPL / size, rest = lane * EPL - g * size;   // of the lane's first expert
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
-        if (!((kept >> (g & 31)) & 1)) key[j] = 0;
+        if (!((kept >> (g & 31)) & 1)) key[j] = kNone;
         if (++rest == size) {
             rest = 0;
             ++g;
@@ -172,57 +177,58 @@ __device__ __forceinline__ void keep_groups(const RouterArgs &a, int lane, uint3
     }
 }
 
-// A token's room in shared memory: the keys (keep_groups) or the candidates.
-__host__ __device__ constexpr int room_of(int E) { return E > 96 ? E : 96; }
+// A token's room in shared memory: the keys (keep_groups), or 32 candidates (key and expert).
+__host__ __device__ constexpr int room_of(int E) { return (E > 64 ? E : 64) + 3 & ~3; }
 
 template <int EPL, bool VEC>
 __global__ void __launch_bounds__(kWarps * 32) route_topk_kernel(RouterArgs a) {
-    extern __shared__ __align__(16) uint32_t rooms[];   // [kWarps][room_of(E)]
+    extern __shared__ __align__(16) float rooms[];   // [kWarps][room_of(E)]
     pdl_begin();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t t = (int64_t)blockIdx.x * kWarps + warp;
     if (t >= a.T) return;
-    uint32_t *room = rooms + warp * room_of(a.E);
-    float l[EPL];
-    uint32_t key[EPL];
-    load_logits<EPL, VEC>(a, t, lane * EPL, l);
-    // s: the score, or the logit where the score is computed for the picks alone
-    float m = 0.f;
-    if (a.by_logit) {
+    float *room = rooms + warp * room_of(a.E);
+    float key[EPL];
+    load_values<EPL, VEC>(logits_row(a, t), a.f32, lane * EPL, a.E, kNone, key);
+    // m, z: what a softmax score is made with, exp(logit - m) / z
+    float m = 0.f, z = 1.f;
+    if (!a.sigmoid || a.by_logit) {
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) key[j] = key_of(l[j]);
-        if (!a.sigmoid) m = row_max<EPL>(l);
+        for (int j = 0; j < EPL; ++j) key[j] = clean(key[j]);
     }
-    float z = 1.f;   // what the picks' scores are divided by, before their own sum
-    if (a.by_logit && !a.sigmoid && !a.renorm) {
-        z = 0.f;
+    if (!a.sigmoid) {
+        m = row_max<EPL>(key);
+        if (!a.renorm || !a.by_logit) {   // the picks' own sum takes z out again
+            z = 0.f;
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) z += expf(l[j] - m);
-        z = fmaxf(warp_sum(z), 1e-38f);
+            for (int j = 0; j < EPL; ++j) z += expf(key[j] - m);
+            z = __fdiv_rn(1.0f, fmaxf(warp_sum(z), 1e-38f));
+        }
     }
     if (!a.by_logit) {
-        float s[EPL];
-        score_row<EPL>(a, l, s);
+        float b[EPL];
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) b[j] = 0.f;
+        if (a.bias) load_values<EPL, VEC>(a.bias, true, lane * EPL, a.E, 0.f, b);
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
-            const int e = lane * EPL + j;
-            const float b = a.bias && e < a.E ? __ldg(a.bias + e) : 0.f;
-            key[j] = key_of(l[j]) ? key_of(__fadd_rn(s[j], b)) : 0;
-            l[j] = s[j];
+            const float s = a.sigmoid ? sigmoid(key[j]) : expf(key[j] - m) * z;
+            // (not a number, of either, is no key)
+            key[j] = key[j] > kNone ? fmaxf(__fadd_rn(s, b[j]), kNone) : kNone;
         }
     }
     if (a.groups > 1) keep_groups<EPL>(a, lane, key, room);
 
-    // the bound: the k-th largest of the lanes' maxima (1, every key there is, if there are fewer)
-    uint32_t best = 0;
+    // the bound: the k-th largest of the lanes' maxima; the lowest number if there are fewer
+    float best = kNone;
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) best = max(best, key[j]);
-    uint32_t bound = 1, rest = best;
+    for (int j = 0; j < EPL; ++j) best = fmaxf(best, key[j]);
+    float bound = -kMost, rest = best;
     for (int i = 0; i < a.k; ++i) {
-        const uint32_t top = __reduce_max_sync(kAllLanes, rest);
-        bound = max(top, 1u);
-        if (top == 0) break;
-        if (rest == top) rest = 0;   // all of its lanes: the bound only gets lower
+        const float top = redux_max(rest);
+        bound = fmaxf(top, -kMost);
+        if (top == kNone) break;
+        if (rest == top) rest = kNone;   // all of its lanes: the bound only gets lower
     }
     int mine = 0;
 #pragma unroll
@@ -235,68 +241,61 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_kernel(RouterArgs a) {
     }
     const int n = __shfl_sync(kAllLanes, at, 31);
     int id = -1, rank = lane;
-    float w = 0.f;
     if (n <= 32) {
         // in the experts' order into shared memory; a lane's candidate comes behind those with a
         // larger key, and behind equal ones before it
-        at -= mine;
+        float *slot = room + (at - mine);
 #pragma unroll
         for (int j = 0; j < EPL; ++j)
             if (key[j] >= bound) {
-                room[at] = key[j];
-                room[32 + at] = __float_as_uint(l[j]);
-                room[64 + at] = lane * EPL + j;
-                ++at;
+                slot[0] = key[j];
+                slot[32] = __int_as_float(lane * EPL + j);
+                ++slot;
             }
+        if (lane >= n) room[lane] = kNone;   // (room up to 32: lanes without a candidate)
         __syncwarp();
-        uint32_t own = 0;
-        if (lane < n) {
-            own = room[lane];
-            w = __uint_as_float(room[32 + lane]);
-            id = (int)room[64 + lane];
-        }
+        const float own = room[lane];
+        if (lane < n) id = __float_as_int(room[32 + lane]);
         int before = 0;
-        for (int i = 0; i < n; ++i) {
-            const uint32_t other = __shfl_sync(kAllLanes, own, i);
-            before += other > own || (other == own && i < lane);
+        for (int i = 0; i < n; i += 4) {
+            const float4 o = *reinterpret_cast<const float4 *>(room + i);
+            before += o.x > own || (o.x == own && i < lane);
+            before += o.y > own || (o.y == own && i + 1 < lane);
+            before += o.z > own || (o.z == own && i + 2 < lane);
+            before += o.w > own || (o.w == own && i + 3 < lane);
         }
-        rank = before;   // lanes without a candidate (key 0) come last, in their own order
-        if (lane >= n) rank = lane;
-        if (rank >= a.k) w = 0.f;
+        rank = lane < n ? before : lane;   // (lanes without a candidate keep the places from n on)
     } else {   // many equal keys, or k near the number of lanes: one by one, pick i to lane i
         for (int i = 0; i < a.k; ++i) {
-            const uint32_t top = __reduce_max_sync(kAllLanes, best);
-            if (top == 0) break;
+            const float top = redux_max(best);
+            if (top == kNone) break;
             const int owner = __ffs(__ballot_sync(kAllLanes, best == top)) - 1;
             int which = -1;
-            float sc = 0.f;
             if (lane == owner) {
-                best = 0;
+                best = kNone;
 #pragma unroll
                 for (int j = 0; j < EPL; ++j) {
                     if (which < 0 && key[j] == top) {
                         which = lane * EPL + j;
-                        sc = l[j];
-                        key[j] = 0;
+                        key[j] = kNone;
                     }
-                    best = max(best, key[j]);
+                    best = fmaxf(best, key[j]);
                 }
             }
             which = __shfl_sync(kAllLanes, which, owner);
-            sc = __shfl_sync(kAllLanes, sc, owner);
-            if (lane == i) {
-                id = which;
-                w = sc;
-            }
+            if (lane == i) id = which;
         }
     }
-    const bool picked = id >= 0 && rank < a.k;
-    if (a.by_logit) w = !picked ? 0.f : a.sigmoid ? sigmoid(w) : __fdiv_rn(expf(w - m), z);
-    if (a.renorm) w = __fdiv_rn(w, fmaxf(warp_sum(w), 1e-38f));
+    float w = 0.f;
+    if (rank < a.k && id >= 0) {   // the pick's score, from its logit
+        const float l = logit(a, t, id);
+        w = a.sigmoid ? sigmoid(l) : expf(l - m) * z;
+    }
+    if (a.renorm) w = __fdividef(w, fmaxf(warp_sum(w), 1e-38f));
     if (rank < a.k) {
         const int64_t o = t * a.k + rank;
-        if (a.ids64) static_cast<int64_t *>(a.ids)[o] = picked ? id : -1;
-        else static_cast<int32_t *>(a.ids)[o] = picked ? id : -1;
+        if (a.ids64) static_cast<int64_t *>(a.ids)[o] = id;
+        else static_cast<int32_t *>(a.ids)[o] = id;
         a.weights[o] = w * a.scale;
     }
 }
@@ -306,12 +305,12 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_kernel(RouterArgs a) {
 //   dlogit = ds s (1 - s) for the sigmoid, s (ds - sum(ds s)) for the softmax.
 template <int EPL, bool VEC>
 __global__ void __launch_bounds__(kWarps * 32) route_topk_backward_kernel(RouterArgs a) {
-    extern __shared__ __align__(16) uint32_t rooms[];   // [kWarps][32 * EPL]
+    extern __shared__ __align__(16) float rooms[];   // [kWarps][32 * EPL]
     pdl_begin();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t t = (int64_t)blockIdx.x * kWarps + warp;
     if (t >= a.T) return;
-    float *room = reinterpret_cast<float *>(rooms) + warp * 32 * EPL;
+    float *room = rooms + warp * 32 * EPL;
     int id = -1;
     float g = 0.f;
     if (lane < a.k) {
@@ -323,7 +322,9 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_backward_kernel(Router
         }
     }
     float l[EPL], s[EPL], d[EPL];
-    load_logits<EPL, VEC>(a, t, lane * EPL, l);
+    load_values<EPL, VEC>(logits_row(a, t), a.f32, lane * EPL, a.E, kNone, l);
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) l[j] = clean(l[j]);
     score_row<EPL>(a, l, s);
     if (a.renorm) {
 #pragma unroll
@@ -435,7 +436,7 @@ cudaError_t with_epl(const RouterArgs &a, F &&f) {
     auto vec = [&](auto epl) {
         constexpr int n = decltype(epl)::value;
         if constexpr (n >= 4) {
-            if (a.E % n == 0 && a.stride % 4 == 0 && is_aligned(a.logits, b) && is_aligned(a.dlogits, b))
+            if (a.E % n == 0 && a.stride % 4 == 0 && is_aligned(a.logits, b) && is_aligned(a.dlogits, b) && is_aligned(a.bias, 16))
                 return f(epl, std::true_type{});
         }
         return f(epl, std::false_type{});
