@@ -25,18 +25,19 @@ struct RouterArgs {
     void *dlogits;
     int64_t stride;          // of logits, in elements
     int T, E, k, sigmoid, groups, top_groups, pair, renorm, f32, ids64, by_logit;
-    int lanes_per_group;     // where a group is a power of two of whole lanes, else 0
+    int lanes_per_group, group_shift;   // where a group is a power of two of whole lanes, else 0; its exponent
     float scale;
 };
 
 constexpr float kNone = -__builtin_huge_valf();   // the key of an absent expert
 constexpr float kMost = 3.402823466e38f;
 
-__device__ __forceinline__ float redux_max(float v) {
-    float r;
-    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
-    return r;
+// An integer that orders as the float does (-0 as +0), and back.
+__device__ __forceinline__ int order_of(float v) {
+    const int i = __float_as_int(v + 0.0f);
+    return i ^ (i >> 31 & 0x7fffffff);
 }
+__device__ __forceinline__ float of_order(int i) { return __int_as_float(i ^ (i >> 31 & 0x7fffffff)); }
 
 // A lane's EPL values of a row, `fill` beyond the last one.  VEC: four at a time; the lanes'
 // experts then all exist or none of them does.
@@ -82,8 +83,21 @@ __device__ __forceinline__ float logit(const RouterArgs &a, int64_t t, int e) {
     return clean(a.f32 ? static_cast<const float *>(row)[e] : __bfloat162float(static_cast<const __nv_bfloat16 *>(row)[e]));
 }
 
-// 1 / (1 + e^-v), the reciprocal to within 1 ulp.
-__device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.0f, 1.0f + expf(-v)); }
+// e^v = 2^(v log2 e): the power of two by the hardware's approximation (to about 1 ulp), and what
+// the product lost in rounding put back.  0 and infinity at the ends.
+__device__ __forceinline__ float exp_of(float v) {
+    constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+    const float t = v * kLog2e;
+    float p;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(t));
+    return t > -126.f && t < 128.f ? fmaf(p, fmaf(v, kLog2e, -t) * kLn2, p) : p;
+}
+// 1 / (1 + e^-v).
+__device__ __forceinline__ float sigmoid(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + exp_of(-v)));
+    return r;
+}
 
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
@@ -111,7 +125,7 @@ __device__ __forceinline__ void score_row(const RouterArgs &a, const float (&l)[
     float z = 0.f;
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
-        s[j] = expf(l[j] - m);
+        s[j] = exp_of(l[j] - m);
         z += s[j];
     }
     z = __fdiv_rn(1.0f, fmaxf(warp_sum(z), 1e-38f));
@@ -137,14 +151,15 @@ __device__ __forceinline__ void keep_groups(const RouterArgs &a, int lane, float
             second = fmaxf(fmaxf(second, s), fminf(first, f));
             first = fmaxf(first, f);
         }
+        // a group's lanes share out the comparisons with the groups
         const float score = a.pair && second > kNone ? first + second : first;
-        const int mine = lane / a.lanes_per_group;
+        const int per = a.lanes_per_group, mine = lane >> a.group_shift;
         int rank = 0;
-#pragma unroll 4
-        for (int g = 0; g < a.groups; ++g) {
-            const float other = __shfl_sync(kAllLanes, score, g * a.lanes_per_group);
-            rank += other > score || (other == score && g < mine);
+        for (int g = lane & (per - 1); g < a.groups + (lane & (per - 1)); g += per) {
+            const float other = __shfl_sync(kAllLanes, score, (g << a.group_shift) & 31);
+            rank += g < a.groups && (other > score || (other == score && g < mine));
         }
+        for (int o = 1; o < per; o <<= 1) rank += __shfl_xor_sync(kAllLanes, rank, o);
         if (rank >= a.top_groups)
 #pragma unroll
             for (int j = 0; j < EPL; ++j) key[j] = kNone;
@@ -201,7 +216,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_kernel(RouterArgs a) {
         if (!a.renorm || !a.by_logit) {   // the picks' own sum takes z out again
             z = 0.f;
 #pragma unroll
-            for (int j = 0; j < EPL; ++j) z += expf(key[j] - m);
+            for (int j = 0; j < EPL; ++j) z += exp_of(key[j] - m);
             z = __fdiv_rn(1.0f, fmaxf(warp_sum(z), 1e-38f));
         }
     }
@@ -210,11 +225,15 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_kernel(RouterArgs a) {
 #pragma unroll
         for (int j = 0; j < EPL; ++j) b[j] = 0.f;
         if (a.bias) load_values<EPL, VEC>(a.bias, true, lane * EPL, a.E, 0.f, b);
+        // (not a number, of either, is no key)
+        if (a.sigmoid) {
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) {
-            const float s = a.sigmoid ? sigmoid(key[j]) : expf(key[j] - m) * z;
-            // (not a number, of either, is no key)
-            key[j] = key[j] > kNone ? fmaxf(__fadd_rn(s, b[j]), kNone) : kNone;
+            for (int j = 0; j < EPL; ++j)
+                key[j] = key[j] > kNone ? fmaxf(__fadd_rn(sigmoid(key[j]), b[j]), kNone) : kNone;
+        } else {
+#pragma unroll
+            for (int j = 0; j < EPL; ++j)
+                key[j] = key[j] > kNone ? fmaxf(__fadd_rn(exp_of(key[j] - m) * z, b[j]), kNone) : kNone;
         }
     }
     if (a.groups > 1) keep_groups<EPL>(a, lane, key, room);
@@ -223,13 +242,13 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_kernel(RouterArgs a) {
     float best = kNone;
 #pragma unroll
     for (int j = 0; j < EPL; ++j) best = fmaxf(best, key[j]);
-    float bound = -kMost, rest = best;
+    const int none = order_of(kNone);
+    int rest = order_of(best), top = none;
     for (int i = 0; i < a.k; ++i) {
-        const float top = redux_max(rest);
-        bound = fmaxf(top, -kMost);
-        if (top == kNone) break;
-        if (rest == top) rest = kNone;   // all of its lanes: the bound only gets lower
+        top = __reduce_max_sync(kAllLanes, rest);
+        if (rest == top) rest = none;   // all of its lanes: the bound only gets lower
     }
+    const float bound = fmaxf(of_order(top), -kMost);
     int mine = 0;
 #pragma unroll
     for (int j = 0; j < EPL; ++j) mine += key[j] >= bound;
@@ -267,7 +286,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_kernel(RouterArgs a) {
         rank = lane < n ? before : lane;   // (lanes without a candidate keep the places from n on)
     } else {   // many equal keys, or k near the number of lanes: one by one, pick i to lane i
         for (int i = 0; i < a.k; ++i) {
-            const float top = redux_max(best);
+            const float top = of_order(__reduce_max_sync(kAllLanes, order_of(best)));
             if (top == kNone) break;
             const int owner = __ffs(__ballot_sync(kAllLanes, best == top)) - 1;
             int which = -1;
@@ -289,7 +308,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_kernel(RouterArgs a) {
     float w = 0.f;
     if (rank < a.k && id >= 0) {   // the pick's score, from its logit
         const float l = logit(a, t, id);
-        w = a.sigmoid ? sigmoid(l) : expf(l - m) * z;
+        w = a.sigmoid ? sigmoid(l) : exp_of(l - m) * z;
     }
     if (a.renorm) w = __fdividef(w, fmaxf(warp_sum(w), 1e-38f));
     if (rank < a.k) {
@@ -424,6 +443,7 @@ RouterArgs router_args(const moe_router *r, int32_t T, const void *logits, const
     while (32 * epl < a.E) epl *= 2;
     const int size = a.E / a.groups, lanes = size / epl;
     a.lanes_per_group = size % epl == 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
+    while (1 << a.group_shift < a.lanes_per_group) ++a.group_shift;
     return a;
 }
 
