@@ -83,14 +83,12 @@ __device__ __forceinline__ float logit(const RouterArgs &a, int64_t t, int e) {
     return clean(a.f32 ? static_cast<const float *>(row)[e] : __bfloat162float(static_cast<const __nv_bfloat16 *>(row)[e]));
 }
 
-// e^v = 2^(v log2 e): the power of two by the hardware's approximation (to about 1 ulp), and what
-// the product lost in rounding put back.  0 and infinity at the ends.
+// e^v as 2^(v log2 e) with the hardware's power of two: relative error 2^-22 for |v| below 1, and
+// 2^-25 |v| more for the rounding of the product.
 __device__ __forceinline__ float exp_of(float v) {
-    constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-    const float t = v * kLog2e;
     float p;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(t));
-    return t > -126.f && t < 128.f ? fmaf(p, fmaf(v, kLog2e, -t) * kLn2, p) : p;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(v * 1.4426950408889634f));
+    return p;
 }
 // 1 / (1 + e^-v).
 __device__ __forceinline__ float sigmoid(float v) {
@@ -225,15 +223,18 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_kernel(RouterArgs a) {
 #pragma unroll
         for (int j = 0; j < EPL; ++j) b[j] = 0.f;
         if (a.bias) load_values<EPL, VEC>(a.bias, true, lane * EPL, a.E, 0.f, b);
-        // (not a number, of either, is no key)
+        // 0 times the logit is not a number for an absent expert, and what is not, for whatever
+        // reason, is no key
         if (a.sigmoid) {
 #pragma unroll
-            for (int j = 0; j < EPL; ++j)
-                key[j] = key[j] > kNone ? fmaxf(__fadd_rn(sigmoid(key[j]), b[j]), kNone) : kNone;
+            for (int j = 0; j < EPL; ++j) {
+                const float l = fminf(key[j], kMost);
+                key[j] = fmaxf(fmaf(l, 0.f, __fadd_rn(sigmoid(key[j]), b[j])), kNone);
+            }
         } else {
 #pragma unroll
             for (int j = 0; j < EPL; ++j)
-                key[j] = key[j] > kNone ? fmaxf(__fadd_rn(exp_of(key[j] - m) * z, b[j]), kNone) : kNone;
+                key[j] = fmaxf(fmaf(key[j], 0.f, __fadd_rn(exp_of(key[j] - m) * z, b[j])), kNone);
         }
     }
     if (a.groups > 1) keep_groups<EPL>(a, lane, key, room);
@@ -249,10 +250,10 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_kernel(RouterArgs a) {
         if (rest == top) rest = none;   // all of its lanes: the bound only gets lower
     }
     const float bound = fmaxf(of_order(top), -kMost);
-    int mine = 0;
+    int count = 0;
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) mine += key[j] >= bound;
-    int at = mine;   // candidates up to this lane's last
+    for (int j = 0; j < EPL; ++j) count += key[j] >= bound;
+    int at = count;   // candidates up to this lane's last
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(kAllLanes, at, o);
@@ -263,7 +264,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_kernel(RouterArgs a) {
     if (n <= 32) {
         // in the experts' order into shared memory; a lane's candidate comes behind those with a
         // larger key, and behind equal ones before it
-        float *slot = room + (at - mine);
+        float *slot = room + (at - count);
 #pragma unroll
         for (int j = 0; j < EPL; ++j)
             if (key[j] >= bound) {
@@ -273,16 +274,21 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_kernel(RouterArgs a) {
             }
         if (lane >= n) room[lane] = kNone;   // (room up to 32: lanes without a candidate)
         __syncwarp();
-        const float own = room[lane];
         if (lane < n) id = __float_as_int(room[32 + lane]);
+        // up to 16: lane c and lane 16 + c compare candidate c with every other four
+        const bool half = n <= 16;
+        const int c = half ? lane & 15 : lane, skip = half ? 8 : 4;
+        const float mine = room[c];
         int before = 0;
-        for (int i = 0; i < n; i += 4) {
+        for (int i = half ? lane >> 4 << 2 : 0; i < n; i += skip) {
             const float4 o = *reinterpret_cast<const float4 *>(room + i);
-            before += o.x > own || (o.x == own && i < lane);
-            before += o.y > own || (o.y == own && i + 1 < lane);
-            before += o.z > own || (o.z == own && i + 2 < lane);
-            before += o.w > own || (o.w == own && i + 3 < lane);
+            before += o.x > mine || (o.x == mine && i < c);
+            before += o.y > mine || (o.y == mine && i + 1 < c);
+            before += o.z > mine || (o.z == mine && i + 2 < c);
+            before += o.w > mine || (o.w == mine && i + 3 < c);
         }
+        const int rest = __shfl_xor_sync(kAllLanes, before, 16);
+        if (half) before += rest;
         rank = lane < n ? before : lane;   // (lanes without a candidate keep the places from n on)
     } else {   // many equal keys, or k near the number of lanes: one by one, pick i to lane i
         for (int i = 0; i < a.k; ++i) {
