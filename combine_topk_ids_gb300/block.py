@@ -120,7 +120,7 @@ def _stream(stream, dev):
     if dev < 0:
         raise ValueError("the tensors are in host memory; expected a CUDA device")
     if stream is None:
-        if torch.cuda.current_device() != dev:
+        if torch._C._cuda_getDevice() != dev:
             raise ValueError("the tensors are on cuda:%d, and the current device is cuda:%d"
                              % (dev, torch.cuda.current_device()))
         return torch._C._cuda_getCurrentRawStream(dev)

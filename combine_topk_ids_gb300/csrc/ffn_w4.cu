@@ -17,8 +17,8 @@
 //     the matrix sum starts;
 //   - the inputs are f16 too: 64 of them at a time are divided by a power of two that brings
 //     the largest to 2^14 .. 2^15 (W4Inputs).  f16 holds the eight bits of x exactly; the
-//     activation is rounded to its eleven, four times finer than out's own rounding.
-// Products are exact, sums float32.  A block takes eight tiles of 16 weight rows; for 128
+//     activation is rounded to its eleven, eight times finer than out's own rounding.
+// Products are exact, sums float32.  A block takes eight tiles of 16 weight rows; for 256
 // inputs at a time one warp copies their codes and scales (contiguous in the prepared order)
 // and the picks' inputs to a ring of stages in shared memory, and eight warps compute: two
 // groups of four, two tiles a warp, take turns at the stages and add up at the end.  (A unit
@@ -85,10 +85,6 @@ __device__ __forceinline__ int load_id(const W4Args &a, int64_t p) {
     const int64_t v = a.ids64 ? static_cast<const int64_t *>(a.ids)[p] : static_cast<const int32_t *>(a.ids)[p];
     return v >= 0 && v < a.E ? (int)v : v == -1 ? -1 : -2;
 }
-
-// The next kernel of the call may be launched: it waits for this one before it touches what
-// this one writes.
-__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // 1 / e and e for the largest magnitude m of 64 inputs.
 __device__ __forceinline__ void power_scale(float m, float &down, float &e) {
@@ -361,7 +357,7 @@ __global__ void __launch_bounds__(kW4Threads, kW4Blocks) w4_product_kernel(W4Arg
     // The first product lets the second one start as blocks of it end: that one's copying warp
     // then fetches weights, which depend on the grouping alone, before it waits for the activation.
     if (UP) pdl_begin();
-    if (UP) pdl_trigger();
+    pdl_trigger();
     const int blocks = (UP ? a.H : a.I) / 128, steps = (blocks + 1) / 2;   // 128 inputs, and stages, of a unit
     const int groups = (UP ? a.I / 8 : a.H / 16) / kW4Tiles;
     const int entries = __ldcg(a.entries_used);

@@ -29,6 +29,7 @@ __global__ void __launch_bounds__(MAXT) add_rmsnorm_backward_kernel(NormBackArgs
     __shared__ float red[2][32];
     extern __shared__ float cols[];   // [H] when blockDim.y > 1
     pdl_begin();
+    pdl_trigger();
     float dw[VPT][8];
 #pragma unroll
     for (int v = 0; v < VPT; ++v)

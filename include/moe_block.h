@@ -173,8 +173,10 @@ int moe_prepare_weights_w4(const moe_w4_geom *g, const uint8_t *w1_codes_dev, co
  *     out[t] = sum over picks j of topk_weights[t, j] * W2_e (silu(Wg_e x[t]) * (Wu_e x[t]))
  *   The same function as moe_dispatch -> moe_expert_ffn -> moe_combine, for batches with few
  *   rows for each expert, whose time is that of reading the picked experts' weights.  Weights
- *   enter the products exactly (integers, scaled in float32); sums are float32; the
- *   activation enters the second product as a bf16 pair; out is rounded once.
+ *   enter the products exactly (integers, scaled in float32) and so does x; the activation is
+ *   rounded to the eleven bits of f16 (with a power of two for each 64 values of a row, so that
+ *   its size does not matter); sums are float32; out is rounded once.  An infinity in a row of x
+ *   makes the token's out not a number.
  *   x_dev, out_dev bf16 [num_tokens, hidden]; topk_ids_dev [num_tokens, top_k]: -1 is a masked
  *   pick, an id outside [-1, num_experts) is dropped and sets MOE_STATUS_BAD_EXPERT_ID.
  *   status_dev: one int32, written by the call (0: clean).  workspace_dev: 256-byte aligned.

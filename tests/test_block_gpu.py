@@ -408,3 +408,38 @@ def test_w4_against_the_bf16_layer():
     ref, bound = ob.forward_w4(f64(x), ids.cpu().numpy(), f64(w), w1.cpu().numpy(), f64(s1), w2.cpu().numpy(), f64(s2))
     within(f64(a.forward(x, ids, w)), ref, bound, "bf16 layer")
     within(f64(b.forward(x, ids, w)), ref, bound, "4-bit layer")
+
+
+def test_w4_rows_of_all_sizes():
+    """Outliers, tiny and empty rows; a row that is not finite spoils its own token alone."""
+    T, H, E, k, I, G = 9, 512, 4, 2, 256, 32
+    case = w4_case(T, H, E, k, I, G, seed=3)
+    layer = w4_layer(T, H, E, k, I, G, case)
+    x, ids, w = case[:3]
+    x[0] = 0
+    x[1, 7] = 3e4
+    x[2] *= 1e-12
+    x[3, ::2] *= 1e-6
+    x[4] *= 1e5
+    layer.forward(x, ids, w)
+    check_w4(layer.out, x, ids, w, case[3:])
+    assert (layer.out[0] == 0).all()
+    want = layer.out.clone()
+    x[5, 3], x[6, 100] = float("nan"), float("inf")
+    out = layer.forward(x, ids, w)
+    assert out[5].isnan().all() and out[6].isnan().all() and layer.status() == 0
+    keep = [t for t in range(T) if t not in (5, 6)]
+    assert torch.equal(out[keep], want[keep])
+
+
+def test_w4_many_picks():
+    """More picks than the blocks count places for themselves, and many rows for each expert."""
+    T, H, E, k, I, G = 310, 256, 6, 4, 128, 64
+    case = w4_case(T, H, E, k, I, G, seed=5)
+    layer = w4_layer(T, H, E, k, I, G, case)
+    x, ids, w = case[:3]
+    ids[::7, 1] = -1
+    out = layer.forward(x, ids, w).clone()
+    assert layer.status() == 0
+    check_w4(out, x, ids, torch.where(ids < 0, torch.zeros_like(w), w), case[3:])
+    assert torch.equal(layer.forward(x[:200], ids[:200].contiguous(), w[:200]), out[:200])
