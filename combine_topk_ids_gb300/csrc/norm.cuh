@@ -2,6 +2,8 @@
 // written eight columns at a time, sums over a row, argument checks.
 #pragma once
 
+#include <mutex>
+
 #include "block_common.cuh"
 
 namespace moe {
@@ -176,6 +178,19 @@ int64_t resident_blocks(int threads) {
     }();
     const int blocks = 65536 / (regs * threads);
     return (int64_t)num_sms() * (blocks < 1 ? 1 : blocks > 2048 / threads ? 2048 / threads : blocks);
+}
+
+// Lets a kernel have `most` bytes of dynamic shared memory (set once for each device).
+template <auto KERNEL>
+cudaError_t allow_smem(size_t most) {
+    static std::once_flag once[64];
+    static cudaError_t set[64];
+    const int dev = device_ordinal();
+    if (dev < 0) return cudaErrorInvalidDevice;
+    std::call_once(once[dev], [&] {
+        set[dev] = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+    });
+    return set[dev];
 }
 
 // Whether a row matrix (or NULL) lies on 16-byte boundaries throughout.

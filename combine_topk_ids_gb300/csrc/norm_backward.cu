@@ -4,7 +4,8 @@
 // With g = dout * w and xhat = h * rstd, one row:
 //     dx = rstd * (g - xhat * mean(g * xhat)) + dsum;     dw += dout * xhat
 // dout, h and dsum are read once, dx is written once; the columns' sums stay in registers over a
-// block's rows and are added up by a second kernel in a fixed order.  HBM bounds it.
+// block's rows and are added up by a second kernel in a fixed order.  HBM bounds it, if enough
+// rows are under way: BACK1
 #include "norm.cuh"
 
 namespace moe {
@@ -21,13 +22,34 @@ struct NormBackArgs {
     int T, H;
 };
 
+// Rows that a thread has under way in shared memory, where they are on 16-byte boundaries and a
+// block's fit: its own columns alone, so that no barrier is needed.
+template <int VPT, bool R32, bool ODD>
+struct Ring {
+    static constexpr bool kUsed = !ODD && VPT == 2;
+    static constexpr int kStages = R32 ? 2 : 3;
+    static constexpr int kHalf = R32 ? 2 : 1;                  // 16-byte pieces of 8 columns of h, dsum
+    static constexpr int kPieces = VPT * (1 + 2 * kHalf);      // of a row, for a thread
+    static size_t bytes(int threads) { return kUsed ? (size_t)kStages * kPieces * threads * 16 : 0; }
+};
+
+__device__ __forceinline__ void copy_16(uint4 *to, const void *from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from)
+                 : "memory");
+}
+
 // Each block takes every gridDim.x-th group of blockDim.y rows and keeps its columns' sums of
-// dout * xhat in registers; they leave as one row of `part`.  A row's inputs are under way
-// while the row before it is computed.  ODD: rows off 16-byte boundaries.
+// dout * xhat in registers; they leave as one row of `part`.  The next rows' inputs are under way
+// (Ring; else the next row's, in registers) while one is computed.  ODD: rows off 16-byte
+// boundaries.
 template <int VPT, int MAXT, bool R32, bool W32, bool ODD>
 __global__ void __launch_bounds__(MAXT) add_rmsnorm_backward_kernel(NormBackArgs a) {
+    using R = Ring<VPT, R32, ODD>;
     __shared__ float red[2][32];
-    extern __shared__ float cols[];   // [H] when blockDim.y > 1
+    extern __shared__ __align__(16) uint4 dynamic[];   // the ring, then [H] floats when blockDim.y > 1
+    const int threads = blockDim.x * blockDim.y;
+    float *cols = reinterpret_cast<float *>(dynamic + (R::kUsed ? R::kStages * R::kPieces * threads : 0));
+    uint4 *mine = dynamic + threadIdx.y * blockDim.x + threadIdx.x;   // piece p of stage s: [(s * kPieces + p) * threads]
     pdl_begin();
     pdl_trigger();
     float dw[VPT][8];
@@ -44,36 +66,71 @@ __global__ void __launch_bounds__(MAXT) add_rmsnorm_backward_kernel(NormBackArgs
     auto h = [&](int64_t t) { return static_cast<const char *>(a.h) + (t < a.T ? t : 0) * a.hs * (R32 ? 4 : 2); };
     auto dsum = [&](int64_t t) { return static_cast<const char *>(a.dsum) + (t < a.T ? t : 0) * a.ss * (R32 ? 4 : 2); };
     auto columns = [&](int64_t t) { return t < a.T ? a.H : 0; };   // rows past the end have none
+    auto column = [&](int v) { return 8 * (int)(threadIdx.x + v * blockDim.x); };
+    // Ring: the pieces of dout, h, dsum of chunk v are v, VPT + kHalf v, VPT + kHalf (VPT + v)
+    auto copy_row = [&](int64_t t, int stage) {
+        uint4 *to = mine + stage * R::kPieces * threads;
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            const int i = column(v);
+            if (i >= columns(t)) continue;
+            copy_16(to + v * threads, dout(t) + i);
+#pragma unroll
+            for (int k = 0; k < R::kHalf; ++k) {
+                copy_16(to + (VPT + R::kHalf * v + k) * threads, h(t) + (int64_t)i * (R32 ? 4 : 2) + 16 * k);
+                if (a.dsum)
+                    copy_16(to + (VPT + R::kHalf * (VPT + v) + k) * threads, dsum(t) + (int64_t)i * (R32 ? 4 : 2) + 16 * k);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    auto take = [&](uint4 (&v)[R::kHalf], int64_t t, int i, const uint4 *from) {
+#pragma unroll
+        for (int k = 0; k < R::kHalf; ++k) v[k] = i < columns(t) ? from[k * threads] : make_uint4(0, 0, 0, 0);
+    };
     auto fetch = [&](int64_t t) {
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
-            const int i = 8 * (int)(threadIdx.x + v * blockDim.x);
-            rg[v].load(dout(t), i, columns(t));
-            rh[v].load(h(t), i, columns(t));
+            rg[v].load(dout(t), column(v), columns(t));
+            rh[v].load(h(t), column(v), columns(t));
         }
     };
     auto fetch_dsum = [&](int64_t t) {
         if (a.dsum)
 #pragma unroll
-            for (int v = 0; v < VPT; ++v) rs[v].load(dsum(t), 8 * (int)(threadIdx.x + v * blockDim.x), columns(t));
+            for (int v = 0; v < VPT; ++v) rs[v].load(dsum(t), column(v), columns(t));
     };
     const int64_t groups = ((int64_t)a.T + blockDim.y - 1) / blockDim.y, step = (int64_t)gridDim.x * blockDim.y;
     int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-    fetch(t);
-    fetch_dsum(t);
+    if constexpr (R::kUsed) {
+        for (int s = 0; s < R::kStages - 1; ++s) copy_row(t + s * step, s);
+    } else {
+        fetch(t);
+        fetch_dsum(t);
+    }
     float rstd = t < a.T ? a.rstd[t] : 0.f;
-    int turn = 0;
+    int turn = 0, stage = 0;
     for (int64_t gr = blockIdx.x; gr < groups; gr += gridDim.x, t += step) {
+        const uint4 *row = mine + stage * R::kPieces * threads;
+        if constexpr (R::kUsed) {
+            copy_row(t + (R::kStages - 1) * step, stage == 0 ? R::kStages - 1 : stage - 1);
+            asm volatile("cp.async.wait_group %0;" ::"n"(R::kStages - 1) : "memory");
+            stage = stage + 1 == R::kStages ? 0 : stage + 1;
+#pragma unroll
+            for (int v = 0; v < VPT; ++v) {
+                rg[v].v[0] = column(v) < columns(t) ? row[v * threads] : make_uint4(0, 0, 0, 0);
+                take(rh[v].v, t, column(v), row + (VPT + R::kHalf * v) * threads);
+            }
+        }
         const float rt = rstd;
         float g[VPT][8], xh[VPT][8];
         float along = 0.f;
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
-            const int i = 8 * (int)(threadIdx.x + v * blockDim.x);
             float w[8];
-            rg[v].floats(dout(t), i, columns(t), g[v]);
-            rh[v].floats(h(t), i, columns(t), xh[v]);
-            rw[v].floats(a.w, i, columns(t), w);
+            rg[v].floats(dout(t), column(v), columns(t), g[v]);
+            rh[v].floats(h(t), column(v), columns(t), xh[v]);
+            rw[v].floats(a.w, column(v), columns(t), w);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 xh[v][j] *= rt;
@@ -82,28 +139,27 @@ __global__ void __launch_bounds__(MAXT) add_rmsnorm_backward_kernel(NormBackArgs
                 along = fmaf(g[v][j], xh[v][j], along);
             }
         }
-        fetch(t + step);
+        if constexpr (!R::kUsed) fetch(t + step);
         rstd = t + step < a.T ? a.rstd[t + step] : 0.f;
         along = row_sum(along, red[turn]) / (float)a.H;   // (two turns: the last row's sums are read until the next barrier)
         turn ^= 1;
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
-            const int i = 8 * (int)(threadIdx.x + v * blockDim.x);
 #pragma unroll
             for (int j = 0; j < 8; ++j) g[v][j] = rt * (g[v][j] - xh[v][j] * along);
             if (a.dsum) {
                 float d[8];
-                rs[v].floats(dsum(t), i, columns(t), d);
+                if constexpr (R::kUsed) take(rs[v].v, t, column(v), row + (VPT + R::kHalf * (VPT + v)) * threads);
+                rs[v].floats(dsum(t), column(v), columns(t), d);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) g[v][j] += d[j];
             }
         }
-        // (dx may be dsum: this row's is read by now, and the next row is another)
-        fetch_dsum(t + step);
+        // (dx may be dsum: this row's is read by now, and the others are other rows)
+        if constexpr (!R::kUsed) fetch_dsum(t + step);
 #pragma unroll
         for (int v = 0; v < VPT; ++v)
-            store8<R32, ODD>(static_cast<char *>(a.dx) + (t < a.T ? t : 0) * a.os * (R32 ? 4 : 2),
-                        8 * (int)(threadIdx.x + v * blockDim.x), columns(t), g[v]);
+            store8<R32, ODD>(static_cast<char *>(a.dx) + (t < a.T ? t : 0) * a.os * (R32 ? 4 : 2), column(v), columns(t), g[v]);
     }
     __syncthreads();
     float *part = a.part + (int64_t)blockIdx.x * a.H;
@@ -198,15 +254,19 @@ int moe_add_rmsnorm_backward(const moe_norm *n, const void *dout_dev, const void
         NormBackArgs a{dout_dev, h_dev, weight_dev, dsum_dev, dx_dev, rstd_dev, part, stride_of(n, n->x_stride),
                        stride_of(n, n->residual_stride), stride_of(n, n->sum_stride),
                        stride_of(n, n->out_stride), n->num_tokens, n->hidden};
-        const size_t smem = sh.rows > 1 ? (size_t)n->hidden * 4 : 0;   // at most 8 KB: rows > 1 below 2048 columns
         const bool odd = n->hidden % 8 || !is_aligned(weight_dev, 16) || !even_rows(dout_dev, a.ds, 2) ||
                          !even_rows(h_dev, a.hs, rb) || !even_rows(dsum_dev, a.ss, rb) || !even_rows(dx_dev, a.os, rb);
         const cudaError_t e = with_shape(
             sh, n->residual_dtype == MOE_DTYPE_FP32, n->weight_dtype == MOE_DTYPE_FP32, odd,
             [&](auto v, auto r32, auto w32, auto odd) {
-                return launch_pdl(add_rmsnorm_backward_kernel<decltype(v)::vpt, decltype(v)::maxt, decltype(r32)::value,
-                                                              decltype(w32)::value, decltype(odd)::value>,
-                                  dim3(blocks), dim3(sh.threads, sh.rows), smem, s, a);
+                using S = decltype(v);
+                constexpr auto kernel = add_rmsnorm_backward_kernel<S::vpt, S::maxt, decltype(r32)::value,
+                                                                    decltype(w32)::value, decltype(odd)::value>;
+                using R = Ring<S::vpt, decltype(r32)::value, decltype(odd)::value>;
+                const size_t cols = sh.rows > 1 ? (size_t)n->hidden * 4 : 0;   // at most 8 KB: rows > 1 up to 2048 columns
+                const cudaError_t set = allow_smem<kernel>(R::bytes(S::maxt) + 8192);
+                if (set != cudaSuccess) return set;
+                return launch_pdl(kernel, dim3(blocks), dim3(sh.threads, sh.rows), R::bytes(sh.threads * sh.rows) + cols, s, a);
             });
         if (e != cudaSuccess) return MOE_ERR_CUDA;
     }

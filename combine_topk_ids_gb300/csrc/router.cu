@@ -336,18 +336,17 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_backward_kernel(Router
     const int64_t t = (int64_t)blockIdx.x * kWarps + warp;
     if (t >= a.T) return;
     float *room = rooms + warp * 32 * EPL;
-    int id = -1;
-    float g = 0.f;
-    if (lane < a.k) {
-        const int64_t o = t * a.k + lane;
-        const int64_t v = a.ids64 ? static_cast<const int64_t *>(a.ids)[o] : static_cast<const int32_t *>(a.ids)[o];
-        if (v >= 0 && v < a.E) {
-            id = (int)v;
-            g = a.weights[o] * a.scale;
-        }
-    }
     float l[EPL], s[EPL], d[EPL];
     load_values<EPL, VEC>(logits_row(a, t), a.f32, lane * EPL, a.E, kNone, l);
+    int64_t v = -1;
+    float g = 0.f;
+    if (lane < a.k) {   // (all the loads are under way together)
+        const int64_t o = t * a.k + lane;
+        v = a.ids64 ? static_cast<const int64_t *>(a.ids)[o] : static_cast<const int32_t *>(a.ids)[o];
+        g = a.weights[o] * a.scale;
+    }
+    const int id = v >= 0 && v < a.E ? (int)v : -1;
+    if (id < 0) g = 0.f;
 #pragma unroll
     for (int j = 0; j < EPL; ++j) l[j] = clean(l[j]);
     score_row<EPL>(a, l, s);
