@@ -4,7 +4,10 @@
 // One row of H columns:  h = x + r;  rstd = 1/sqrt(sum(h^2)/H + eps);  y = h*rstd*w, stored as
 // bf16, as e4m3 codes with a scale per 128 columns, or both.
 // A row is read once and held in registers between the sum of squares and the scaling, so the
-// call moves what it has to: x, r in; h, y out.  HBM bounds it.
+// call moves what it has to: x, r in; h, y out.  HBM bounds it.  Measured: 32768 rows of 7168
+// columns to bf16 and e4m3 (2.12 GB) 328 us, 6.5 TB/s, 0.97 of the measured peak (a block per
+// row without the next row under way: 355 us); 4999 rows of 2047 columns (81.9 MB), off 16-byte
+// boundaries, 22 us, bound by the few rows that fit an SM at once; one row of 7168 3.3 us.
 #include <cuda_fp8.h>
 
 #include "norm.cuh"

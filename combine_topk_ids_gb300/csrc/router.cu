@@ -10,6 +10,12 @@
 // So the k largest keys are not taken out one by one: the k-th largest of the lanes' maxima is
 // a bound that few keys reach (about 11 for k = 8 of 256); these are put together in shared
 // memory and ranked against each other, one to a lane.
+//
+// Measured, 256 experts, sigmoid, bias, 4 of 8 groups by pairs, k = 8: 64 tokens 2.6 us, 32768
+// tokens (37 MB) 21 us: 0.26 of HBM, the schedulers issue in 86% of the cycles (taking the k
+// largest out one by one: 65 us).  16381 tokens of 128 experts, softmax, k = 4: 6.6 us.  The
+// gradient at 32768 x 256 (70 MB): 13.7 us, 0.77 of HBM; the loads' latency, once for each token's
+// warp, is the rest.
 #include "block_common.cuh"
 
 namespace moe {
