@@ -503,7 +503,7 @@ int moe_route_topk(const moe_router *r, int32_t num_tokens, const void *logits_d
     const size_t smem = (size_t)kWarps * room_of(a.E) * 4;   // at most 32 KB
     return status_of(with_epl(a, [&](auto epl, auto vec) {
         return launch_pdl(route_topk_kernel<decltype(epl)::value, decltype(vec)::value>,
-                          dim3((a.T + kWarps - 1) / kWarps), dim3(kWarps * 32), smem,
+                          dim3((a.T - 1) / kWarps + 1), dim3(kWarps * 32), smem,
                           static_cast<cudaStream_t>(stream), a);
     }));
 }
@@ -524,7 +524,7 @@ int moe_route_topk_backward(const moe_router *r, int32_t num_tokens, const void 
                                      dlogits_dev);
     return status_of(with_epl(a, [&](auto epl, auto vec) {
         constexpr int n = decltype(epl)::value;
-        return launch_pdl(route_topk_backward_kernel<n, decltype(vec)::value>, dim3((a.T + kWarps - 1) / kWarps),
+        return launch_pdl(route_topk_backward_kernel<n, decltype(vec)::value>, dim3((a.T - 1) / kWarps + 1),
                           dim3(kWarps * 32), (size_t)kWarps * 32 * n * 4, static_cast<cudaStream_t>(stream), a);
     }));
 }
