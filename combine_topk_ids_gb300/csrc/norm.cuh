@@ -14,12 +14,9 @@ namespace {
 // outside [0, H).
 // ODD: the row may start anywhere and be of any length (else everything is on 16-byte
 // boundaries, and i is a multiple of 8).  What load() cannot fetch, floats() reads one by one.
-// WIN (with ODD): columns off a boundary come with the aligned 16 bytes around them, if these
-// are columns of the row too, and floats() moves them into place.
-template <bool F32, bool ODD, bool WIN = false>
+template <bool F32, bool ODD>
 struct Raw8 {
-    static constexpr int kSize = F32 ? 4 : 2, kPer = 16 / kSize;   // columns in 16 bytes
-    static constexpr int kVecs = (F32 ? 2 : 1) + (WIN ? 1 : 0);
+    static constexpr int kSize = F32 ? 4 : 2, kVecs = F32 ? 2 : 1;
     uint4 v[kVecs];
 
     // Columns by which column i lies behind a 16-byte boundary.
@@ -27,21 +24,16 @@ struct Raw8 {
         return ODD ? (int)((reinterpret_cast<uintptr_t>(row) + (int64_t)i * kSize) & 15) / kSize : 0;
     }
     static __device__ __forceinline__ bool loads(const void *row, int i, int H) {
-        if (!ODD) return i < H;
-        const int r = behind(row, i);
-        if (!WIN) return i >= 0 && i + 8 <= H && r == 0;
-        return i >= r && i - r + (r ? 8 + kPer : 8) <= H;
+        return ODD ? i >= 0 && i + 8 <= H && behind(row, i) == 0 : i < H;
     }
     __device__ __forceinline__ void load(const void *row, int i, int H) {
         if (!ODD)
 #pragma unroll
             for (int k = 0; k < kVecs; ++k) v[k] = make_uint4(0, 0, 0, 0);
         if (loads(row, i, H)) {
-            const int r = WIN ? behind(row, i) : 0;
-            const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const char *>(row) + (int64_t)(i - r) * kSize);
+            const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const char *>(row) + (int64_t)i * kSize);
 #pragma unroll
-            for (int k = 0; k < kVecs; ++k)
-                if (!WIN || k < kVecs - 1 || r) v[k] = p[k];
+            for (int k = 0; k < kVecs; ++k) v[k] = p[k];
         }
     }
     __device__ __forceinline__ void floats(const void *row, int i, int H, float (&f)[8]) const {
@@ -49,19 +41,6 @@ struct Raw8 {
 #pragma unroll
         for (int k = 0; k < kVecs; ++k) {
             w[4 * k] = v[k].x; w[4 * k + 1] = v[k].y; w[4 * k + 2] = v[k].z; w[4 * k + 3] = v[k].w;
-        }
-        if (WIN) {   // r columns on, in steps of 4, 2 and 1
-            const int r = behind(row, i);
-            constexpr int n = 4 * kVecs;
-            if (!F32 && r & 4)
-#pragma unroll
-                for (int k = 0; k + 2 < n; ++k) w[k] = w[k + 2];
-            if (r & 2)
-#pragma unroll
-                for (int k = 0; k + (F32 ? 2 : 1) < n; ++k) w[k] = w[k + (F32 ? 2 : 1)];
-            if (r & 1)
-#pragma unroll
-                for (int k = 0; k + 1 < n; ++k) w[k] = F32 ? w[k + 1] : __funnelshift_r(w[k], w[k + 1], 16);
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j)

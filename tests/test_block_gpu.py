@@ -151,6 +151,36 @@ def test_norm_backward(T, H, stream, weight, dsum):
     assert torch.equal(dw, first)   # the same order of sums every time
 
 
+@pytest.mark.parametrize("T,H,lead,off", [
+    (700, 257, (257, 257, 257), (0, 0, 0)),       # more rows than blocks, each off a boundary in its own way
+    (5000, 133, (133, 133, 133), (0, 0, 0)),      # the same with several rows in a block
+    (650, 4097, (4097, 4097, 4097), (0, 0, 0)),
+    (330, 8201, (8203, 8203, 8203), (1, 1, 1)),
+    (611, 512, (513, 640, 640), (1, 0, 0)),       # dout alone is off the boundaries
+    (611, 512, (640, 513, 515), (0, 1, 3)),       # all but dout
+    (611, 512, (517, 521, 640), (5, 2, 8)),       # each otherwise
+    (9, 5, (5, 9, 6), (0, 4, 1))])
+@pytest.mark.parametrize("stream", [BF, F32])
+def test_norm_backward_strided_rows(T, H, lead, off, stream):
+    """Rows inside wider rows that start anywhere (dout's, h's, and those of dsum, which dx takes
+    the place of); the columns around them keep their values."""
+    wide = [rnd(T, lead[0], seed=3), rnd(T, lead[1], dtype=stream, scale=2, seed=1),
+            rnd(T, lead[2], dtype=stream, seed=4)]
+    dout, h, ds = (m[:, o:o + H] for m, o in zip(wide, off))
+    keep = [m.clone() for m in wide]
+    w = 1 + rnd(H, dtype=F32, scale=0.2, seed=2)
+    rstd = torch.rsqrt(h.double().square().mean(1) + 1e-6).float()
+    dw = torch.empty(H, device="cuda")
+    ws = torch.full((moe.moe_add_rmsnorm_workspace_size(T, H),), 255, dtype=torch.uint8, device="cuda")
+    rx, rw, bx, bw = ob.add_rmsnorm_backward(f64(dout), f64(h), f64(w), f64(rstd), f64(ds))
+    moe.moe_add_rmsnorm_backward(dout, h, w, rstd, ds, dw, ws, dsum=ds)
+    within(f64(ds), rx, bx + (ob.BF16 if stream == BF else 0) * np.abs(rx) + 1e-38, "dx")
+    within(f64(dw), rw, bw + 1e-38, "dweight")
+    assert torch.equal(wide[0], keep[0]) and torch.equal(wide[1], keep[1])
+    assert torch.equal(wide[2][:, :off[2]], keep[2][:, :off[2]])
+    assert torch.equal(wide[2][:, off[2] + H:], keep[2][:, off[2] + H:])
+
+
 def test_norm_backward_against_differences():
     """The GPU's gradient against central differences of the float64 forward."""
     T, H, eps, step = 3, 40, 1e-6, 1e-6
