@@ -155,12 +155,13 @@ __device__ __forceinline__ void store_part(void *row, int i, int H, int lie, con
     }
 }
 
-// Rows that a thread has under way in shared memory, where a block's fit: its own columns alone,
-// so that no barrier is needed.
+// Rows that a thread has under way in shared memory, where a block's fit (up to 16384 columns of
+// bf16, 8192 of float32): its own columns alone, so that no barrier is needed.  2000 rows of 12000
+// columns 59 us, 92 with the next row in registers, which then spill.
 template <int VPT, bool R32>
 struct Ring {
-    static constexpr bool kUsed = VPT == 2;
-    static constexpr int kStages = R32 ? 2 : 3;
+    static constexpr bool kUsed = VPT == 2 || (VPT == 4 && !R32);
+    static constexpr int kStages = R32 || VPT == 4 ? 2 : 3;
     static constexpr int kHalf = R32 ? 2 : 1;                  // 16-byte pieces of 8 columns of h, dsum
     static constexpr int kPieces = VPT * (1 + 2 * kHalf);      // of a row, for a thread
     static size_t bytes(int threads) { return kUsed ? (size_t)kStages * kPieces * threads * 16 : 0; }

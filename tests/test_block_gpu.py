@@ -156,6 +156,8 @@ def test_norm_backward(T, H, stream, weight, dsum):
     (5000, 133, (133, 133, 133), (0, 0, 0)),      # the same with several rows in a block
     (650, 4097, (4097, 4097, 4097), (0, 0, 0)),
     (330, 8201, (8203, 8203, 8203), (1, 1, 1)),
+    (950, 8201, (8201, 8201, 8201), (0, 0, 0)),   # four rows to some blocks
+    (950, 8208, (8208, 8216, 8208), (0, 0, 0)),   # on the boundaries
     (611, 512, (513, 640, 640), (1, 0, 0)),       # dout alone is off the boundaries
     (611, 512, (640, 513, 515), (0, 1, 3)),       # all but dout
     (611, 512, (517, 521, 640), (5, 2, 8)),       # each otherwise
