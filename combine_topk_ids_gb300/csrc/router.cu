@@ -117,7 +117,8 @@ __device__ __forceinline__ float row_max(const float (&l)[EPL]) {
 }
 
 // Scores of a lane's experts.  Softmax over the whole row, with the row's maximum taken out
-// before the exponential; a row with no expert has all scores 0.
+// before the exponential, and undivided where the picks' own sum takes its sum out again; a row
+// with no expert has all scores 0.
 template <int EPL>
 __device__ __forceinline__ void score_row(const RouterArgs &a, const float (&l)[EPL], float (&s)[EPL]) {
     if (a.sigmoid) {
@@ -132,6 +133,7 @@ __device__ __forceinline__ void score_row(const RouterArgs &a, const float (&l)[
         s[j] = exp_of(l[j] - m);
         z += s[j];
     }
+    if (a.renorm) return;
     z = __fdiv_rn(1.0f, fmaxf(warp_sum(z), 1e-38f));
 #pragma unroll
     for (int j = 0; j < EPL; ++j) s[j] *= z;
@@ -331,9 +333,12 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_kernel(RouterArgs a) {
     }
 }
 
-// With p the picked scores, z their sum and g = scale * dweights:
-//   ds = g, or (g - sum(g p)/z)/z where renormalised (0 outside the picks);
-//   dlogit = ds s (1 - s) for the sigmoid, s (ds - sum(ds s)) for the softmax.
+// With s the scores, g = scale * dweights, and q = s / (the picks' sum of s) the picks' shares:
+//   sigmoid   dlogit = s (1 - s) g at the picks, or where renormalised q (1 - s) (g - sum(g q));
+//   softmax   s (d - sum(d s)) with d = g at the picks and 0 elsewhere, or where renormalised
+//             q (g - sum(g q)) at the picks: the softmax's own sum takes no part.
+// The shares are formed first, 0 where the sum is 0: nothing is divided by a sum that may be as
+// small as a score.
 template <int EPL, bool VEC>
 __global__ void __launch_bounds__(kWarps * 32) route_topk_backward_kernel(RouterArgs a) {
     extern __shared__ __align__(16) float rooms[];   // [kWarps][32 * EPL]
@@ -362,9 +367,10 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_backward_kernel(Router
         __syncwarp();
         const float p = id >= 0 ? room[id] : 0.f;   // the score of this lane's pick
         __syncwarp();
-        const float z = fmaxf(warp_sum(p), 1e-38f);
-        const float along = __fdiv_rn(warp_sum(g * p), z);
-        g = id >= 0 ? __fdiv_rn(g - along, z) : 0.f;
+        const float z = warp_sum(p);
+        const float q = p * __fdiv_rn(1.0f, z > 0.f ? z : 1.0f);   // (scores are 0 or at least 2^-126: finite)
+        if (!(p > 0.f)) g = 0.f;   // (an absent expert's weight's gradient may be anything)
+        g = q * (g - warp_sum(g * q));
     }
     // the picks' gradients to the experts' lanes; picks of one expert add up in their order
 #pragma unroll
@@ -382,16 +388,19 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_backward_kernel(Router
     __syncwarp();
 #pragma unroll
     for (int j = 0; j < EPL; ++j) d[j] = room[lane * EPL + j];
+    if (!a.renorm)   // (absent experts as above)
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) d[j] = s[j] > 0.f ? d[j] * s[j] : 0.f;
     if (a.sigmoid) {
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) d[j] = d[j] * s[j] * (1.0f - s[j]);
-    } else {
+        for (int j = 0; j < EPL; ++j) d[j] *= 1.0f - s[j];
+    } else if (!a.renorm) {
         float along = 0.f;
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) along = fmaf(d[j], s[j], along);
+        for (int j = 0; j < EPL; ++j) along += d[j];
         along = warp_sum(along);
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) d[j] = s[j] * (d[j] - along);
+        for (int j = 0; j < EPL; ++j) d[j] = fmaf(-along, s[j], d[j]);
     }
     const int first = lane * EPL;
     if (VEC) {
