@@ -322,9 +322,12 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_kernel(RouterArgs a) {
     float w = 0.f;
     if (rank < a.k && id >= 0) {   // the pick's score, from its logit
         const float l = logit(a, t, id);
-        w = a.sigmoid ? sigmoid(l) : exp_of(l - m) * z;
+        w = a.sigmoid ? sigmoid(l) : exp_of(l - m);
+        // The softmax's own sum would only be taken out again, and what it makes of small scores
+        // lies below float32's normal numbers.
+        if (!a.sigmoid && !a.renorm) w *= z;
     }
-    if (a.renorm) w = __fdividef(w, fmaxf(warp_sum(w), 1e-38f));
+    if (a.renorm) w = __fdividef(w, fmaxf(warp_sum(w), 1e-38f));   // (the sum is 0 or at least 2^-126)
     if (rank < a.k) {
         const int64_t o = t * a.k + rank;
         if (a.ids64) static_cast<int64_t *>(a.ids)[o] = id;

@@ -117,7 +117,8 @@ typedef struct {
  *   keys go to the lowest index, equal groups to the lowest group.
  *   An expert whose logit or bias is -infinity or not a number is absent: it has score 0 and
  *   is never picked.  Picks that find no expert get id -1 and weight 0, which moe_dispatch
- *   and moe_forward_w4 skip.  Where the picked scores' sum is 0 the weights are 0.
+ *   and moe_forward_w4 skip.  Where the picked scores' sum is 0 the weights are 0 (scores are
+ *   float32: one below 2^-126, of a softmax before its division, counts as 0).
  *   topk_ids_dev int32 or int64 [num_tokens, top_k]; topk_weights_dev float32.
  *   Errors: MOE_ERR_INVALID_ARGUMENT (NULL, a bad enum, a stride below num_experts, groups
  *   that do not divide num_experts, top_groups outside [1, groups]), MOE_ERR_TOPK (top_k
