@@ -89,19 +89,20 @@ __device__ __forceinline__ float logit(const RouterArgs &a, int64_t t, int e) {
     return clean(a.f32 ? static_cast<const float *>(row)[e] : __bfloat162float(static_cast<const __nv_bfloat16 *>(row)[e]));
 }
 
-// e^v as 2^(v log2 e) with the hardware's power of two: relative error 2^-22 for |v| below 1, and
-// 2^-25 |v| more for the rounding of the product.
+// e^v as 2^(v log2 e) with the hardware's power of two: relative error 2^-22, and |v| 2^-23 at
+// most for the roundings of the product and of log2 e.
 __device__ __forceinline__ float exp_of(float v) {
     float p;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(v * 1.4426950408889634f));
     return p;
 }
-// 1 / (1 + e^-v).
-__device__ __forceinline__ float sigmoid(float v) {
+__device__ __forceinline__ float reciprocal(float v) {
     float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + exp_of(-v)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
 }
+// 1 / (1 + e^-v).
+__device__ __forceinline__ float sigmoid(float v) { return reciprocal(1.0f + exp_of(-v)); }
 
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
@@ -116,14 +117,16 @@ __device__ __forceinline__ float row_max(const float (&l)[EPL]) {
     return warp_max(m);
 }
 
-// Scores of a lane's experts.  Softmax over the whole row, with the row's maximum taken out
-// before the exponential, and undivided where the picks' own sum takes its sum out again; a row
-// with no expert has all scores 0.
+// What the gradient keeps of a lane's experts.  Softmax: the scores, over the whole row, with its
+// maximum taken out before the exponential, and undivided where the picks' own sum takes the
+// row's out again; a row with no expert has all scores 0.  Sigmoid: u = e^-logit, at most the
+// largest finite number, from which s = 1 / (1 + u), and 1 - s = u s with all its digits where s
+// is next to 1.
 template <int EPL>
 __device__ __forceinline__ void score_row(const RouterArgs &a, const float (&l)[EPL], float (&s)[EPL]) {
     if (a.sigmoid) {
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) s[j] = sigmoid(l[j]);
+        for (int j = 0; j < EPL; ++j) s[j] = fminf(exp_of(-l[j]), kMost);
         return;
     }
     const float m = row_max<EPL>(l);
@@ -366,7 +369,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_backward_kernel(Router
     score_row<EPL>(a, l, s);
     if (a.renorm) {
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) room[lane * EPL + j] = s[j];
+        for (int j = 0; j < EPL; ++j) room[lane * EPL + j] = a.sigmoid ? reciprocal(1.0f + s[j]) : s[j];
         __syncwarp();
         const float p = id >= 0 ? room[id] : 0.f;   // the score of this lane's pick
         __syncwarp();
@@ -391,16 +394,20 @@ __global__ void __launch_bounds__(kWarps * 32) route_topk_backward_kernel(Router
     __syncwarp();
 #pragma unroll
     for (int j = 0; j < EPL; ++j) d[j] = room[lane * EPL + j];
-    if (!a.renorm)   // (absent experts as above)
-#pragma unroll
-        for (int j = 0; j < EPL; ++j) d[j] = s[j] > 0.f ? d[j] * s[j] : 0.f;
     if (a.sigmoid) {
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) d[j] *= 1.0f - s[j];
+        for (int j = 0; j < EPL; ++j) {
+            const float r = reciprocal(1.0f + s[j]);
+            d[j] *= s[j] * r;
+            if (!a.renorm) d[j] = r > 0.f ? d[j] * r : 0.f;   // (absent experts as above)
+        }
     } else if (!a.renorm) {
         float along = 0.f;
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) along += d[j];
+        for (int j = 0; j < EPL; ++j) {
+            d[j] = s[j] > 0.f ? d[j] * s[j] : 0.f;
+            along += d[j];
+        }
         along = warp_sum(along);
 #pragma unroll
         for (int j = 0; j < EPL; ++j) d[j] = fmaf(-along, s[j], d[j]);

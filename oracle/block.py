@@ -127,8 +127,8 @@ def route_backward(logits, ids, dw, kind, renorm, scale):
         rows = np.nonzero(ok[:, j])[0]
         d[rows, ids[rows, j]] += g[rows, j]
         m[rows, ids[rows, j]] += size[rows, j]
-    if kind == "sigmoid":
-        return d * s * (1 - s), 60 * EPS32 * m * s
+    if kind == "sigmoid":   # 1 - s is the sigmoid of -logit, which cancels nothing
+        return d * s * scores(-logits, kind)[0], 60 * EPS32 * m * s
     return s * (d - (d * s).sum(1, keepdims=True)), 60 * EPS32 * s * (m + (m * s).sum(1, keepdims=True))
 
 
