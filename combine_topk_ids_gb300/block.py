@@ -302,9 +302,10 @@ class MoELayerW4:
         if None in natural:
             raise ValueError("w1, s1, w2 and s2 must be given")
         s = _stream(None, dev)
-        self.weights = [torch.empty_like(t) for t, _, _, _ in given]
-        self._addresses = [t.data_ptr() for t in self.weights]
-        _call(_lib().moe_prepare_weights_w4(g, *natural, *self._addresses, s), "moe_prepare_weights_w4")
+        weights = [torch.empty_like(t) for t, _, _, _ in given]
+        addresses = [t.data_ptr() for t in weights]
+        _call(_lib().moe_prepare_weights_w4(g, *natural, *addresses, s), "moe_prepare_weights_w4")
+        self.weights, self._addresses = weights, addresses   # (the old ones stay where the call was refused)
 
     def quantize_weights(self, w1, w2):
         """set_weights from bf16 w1 [E, 2I, H] and w2 [E, H, I]."""
