@@ -623,15 +623,21 @@ __global__ void __launch_bounds__(256) w4_order_scales_kernel(const uint16_t *sc
     out[v] = scales[r0 * (K / G) + at] | (uint32_t)scales[r1 * (K / G) + at] << 16;
 }
 
-// One thread per group.
+// One thread per group.  A group that holds an infinity or NaN has no scale: it gets NaN, so that
+// its weights are NaN, and code 8.
 __global__ void __launch_bounds__(256) w4_quantize_kernel(const uint16_t *w, uint8_t *codes, uint16_t *scales,
                                                           int64_t n, int G) {
     const int64_t v = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (v >= n) return;
     const uint32_t *src = reinterpret_cast<const uint32_t *>(w + v * G);
     float m = 0.f;
-    for (int i = 0; i < G / 2; ++i) m = fmaxf(m, fmaxf(fabsf(lo_f32(src[i])), fabsf(hi_f32(src[i]))));
-    const __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(m, 7.0f));
+    bool finite = true;
+    for (int i = 0; i < G / 2; ++i) {
+        const float a = fabsf(lo_f32(src[i])), b = fabsf(hi_f32(src[i]));
+        finite = finite && a < __builtin_huge_valf() && b < __builtin_huge_valf();
+        m = fmaxf(m, fmaxf(a, b));
+    }
+    const __nv_bfloat16 sb = __float2bfloat16_rn(finite ? __fdiv_rn(m, 7.0f) : __builtin_nanf(""));
     const float s = __bfloat162float(sb);
     scales[v] = __bfloat16_as_ushort(sb);
     auto code = [&](float f) { return s > 0.f ? 8 + (int)fminf(fmaxf(rintf(__fdiv_rn(f, s)), -8.f), 7.f) : 8; };

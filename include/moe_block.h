@@ -153,6 +153,7 @@ typedef struct {
 /*
  * moe_quantize_w4 - bf16 [rows, cols] to codes and scales: scale = bf16(amax / 7) over each
  *   group, code = 8 + clamp(rint(w / scale), -8, 7); a group of zeros gets scale 0, code 8.
+ *   A group with an infinity or NaN among its weights gets scale NaN, code 8: its weights are NaN.
  *   cols % group == 0, rows * cols < 2^62.
  */
 int moe_quantize_w4(int64_t rows, int64_t cols, int32_t group, const void *w_dev, uint8_t *codes_dev,
