@@ -5,8 +5,8 @@ moe_add_rmsnorm / moe_add_rmsnorm_backward, moe_route_topk / moe_route_topk_back
 which owns one layer's weights and buffers.  Argument checks and marshalling only; results
 go to the caller's tensors, on the current stream or the one given.
 
-A row matrix may have any row stride (its columns are packed); every other tensor is
-contiguous.  A tensor of another type raises TypeError, one of another shape, layout or
+The norm's row matrices and the router's logits may have any row stride (their columns are
+packed); every other tensor is contiguous.  A tensor of another type raises TypeError, one of another shape, layout or
 device ValueError, and what the library refuses MoeError.
 """
 import ctypes
@@ -273,9 +273,9 @@ def moe_forward_w4_workspace_size(g):
 class MoELayerW4:
     """The routed experts of one layer with 4-bit weights, for batches of up to `max_tokens`.
 
-    forward(x, topk_ids, topk_weights) -> out [T, H] bf16, the function of MoELayer1GPU.forward,
-    on the current stream and with no host synchronisation.  group: inputs per scale (32, 64
-    or 128).  The buffers (out among them) are the layer's own and are written by every call.
+    forward(x, topk_ids, topk_weights) -> out [T, H] bf16, the function of MoELayer1GPU.forward
+    with the activation in the eleven bits of f16 (there by default a pair of bf16), on the
+    current stream and with no host synchronisation.  group: inputs per scale (32, 64 or 128).  The buffers (out among them) are the layer's own and are written by every call.
     """
 
     def __init__(self, max_tokens, hidden, num_experts, top_k, intermediate, group=128, device="cuda"):

@@ -16,7 +16,8 @@
 //   - the 8 that a code is above its weight comes off through the sums of the inputs, where
 //     the matrix sum starts;
 //   - the inputs are f16 too: 64 of them at a time are divided by a power of two that brings
-//     the largest to 2^14 .. 2^15 (W4Inputs).  f16 holds the eight bits of x exactly; the
+//     the largest to 2^14 .. 2^15 (W4Inputs).  f16 holds the eight bits of x exactly
+//     (while the 64 lie within 2^32 of each other; below that, to 2^-39 of the largest); the
 //     activation is rounded to its eleven, eight times finer than out's own rounding.
 // Products are exact, sums float32.  A block takes eight tiles of 16 weight rows; for 256
 // inputs at a time one warp copies their codes and scales (contiguous in the prepared order)
@@ -624,7 +625,8 @@ __global__ void __launch_bounds__(256) w4_order_scales_kernel(const uint16_t *sc
 }
 
 // One thread per group.  A group that holds an infinity or NaN has no scale: it gets NaN, so that
-// its weights are NaN, and code 8.
+// its weights are NaN, and code 8.  (Done once for a model's weights, and not tuned: 939 M weights,
+// a scale per 128, 5.1 ms against 0.35 for their bytes; neighbouring threads read 256 bytes apart.)
 __global__ void __launch_bounds__(256) w4_quantize_kernel(const uint16_t *w, uint8_t *codes, uint16_t *scales,
                                                           int64_t n, int G) {
     const int64_t v = (int64_t)blockIdx.x * 256 + threadIdx.x;

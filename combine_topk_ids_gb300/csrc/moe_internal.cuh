@@ -105,10 +105,16 @@ int device_ordinal();   // the current device, or -1 (only ordinals below 64 are
 // a kernel is processed while the previous one in the stream runs and its CTAs start as
 // soon as that kernel has finished.  Each kernel waits (pdl_wait) until the previous one
 // has completed and its memory is visible before it touches global memory; the GEMMs set
-// up barriers and tensor memory first.  No kernel triggers its dependents early
+// up barriers and tensor memory first.  No kernel of the layer triggers its dependents early
 // (griddepcontrol.launch_dependents): measured on GB300, an early trigger saved 3% on the
 // 64-token batch but cost 3% on the 1024-token Mixtral-like batch under graph replay.
 // The data order is the plain stream order.
+// The norm's gradient and the 4-bit FFN do trigger, within a call and never in its last kernel
+// (but for an empty 4-bit batch, whose grouping kernel is the only one).  Each block triggers
+// after its own wait, so that where a kernel has started, all before its predecessor has
+// completed.  The 4-bit FFN's second product relies on that: before it waits it reads the
+// weights and the grouping's entries, which the first product has waited for, and nothing that
+// the first product writes.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_begin() { pdl_wait(); }
 

@@ -5,9 +5,14 @@
 // bf16, as e4m3 codes with a scale per 128 columns, or both.
 // A row is read once and held in registers between the sum of squares and the scaling, so the
 // call moves what it has to: x, r in; h, y out.  HBM bounds it.  Measured: 32768 rows of 7168
-// columns to bf16 and e4m3 (2.12 GB) 328 us, 6.5 TB/s, 0.97 of the measured peak (a block per
-// row without the next row under way: 355 us); 4999 rows of 2047 columns (81.9 MB), off 16-byte
-// boundaries, 22 us, bound by the few rows that fit an SM at once; one row of 7168 3.3 us.
+// columns to bf16 and e4m3 (2.12 GB) 330 us, 6.4 TB/s, 0.96 of the measured peak (a block per
+// row without the next row under way: 355 us); to bf16 alone 296 us (0.95), with a float32 stream
+// 454 us (0.93); one row of 7168 3.3 us.
+// 4999 rows of 2047 columns (81.9 MB), off 16-byte boundaries, 22 us (0.55): no unit is full.  8
+// blocks of 160 threads fit an SM (48 registers), the schedulers issue in 66% of the active
+// cycles, the load pipe is busy in 57%, and the longest stall is for loads: latency and
+// instructions share the time.  Above 16384 columns a block of 1024 threads has 64 registers for 64
+// columns a thread and keeps a part of the row in local memory: 1000 rows of 20000 112 us (0.21).
 #include <cuda_fp8.h>
 
 #include "norm.cuh"

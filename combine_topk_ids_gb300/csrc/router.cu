@@ -13,9 +13,10 @@
 //
 // Measured, 256 experts, sigmoid, bias, 4 of 8 groups by pairs, k = 8: 64 tokens 2.6 us, 32768
 // tokens (37 MB) 21 us: 0.26 of HBM, the schedulers issue in 86% of the cycles (taking the k
-// largest out one by one: 65 us).  16381 tokens of 128 experts, softmax, k = 4: 6.6 us.  The
-// gradient at 32768 x 256 (70 MB): 13.7 us, 0.77 of HBM; the loads' latency, once for each token's
-// warp, is the rest.
+// largest out one by one: 65 us).  16381 tokens of 128 experts, softmax, k = 4: 6.7 us; 32768 of 8
+// experts, k = 2: 10.6 us, since a token takes a warp however few its experts are.  The gradient at
+// 32768 x 256 (70 MB): 13.6 us, 0.77 of HBM (sigmoid 12.0, renormalised 14.2); the loads' latency,
+// once for each token's warp, is the rest.
 #include "block_common.cuh"
 
 namespace moe {

@@ -115,10 +115,13 @@ typedef struct {
  *   Without a bias, and without groups or with MOE_GROUP_MAX, the experts are picked by their
  *   logits (both scores rise with the logit).  Picks are in falling order of their keys; equal
  *   keys go to the lowest index, equal groups to the lowest group.
- *   An expert whose logit or bias is -infinity or not a number is absent: it has score 0 and
- *   is never picked.  Picks that find no expert get id -1 and weight 0, which moe_dispatch
+ *   An expert whose logit is -infinity or not a number is absent: it has score 0 and is never
+ *   picked.  One whose bias is -infinity or not a number is never picked either; its logit still
+ *   counts in a softmax's sum.  Picks that find no expert get id -1 and weight 0, which moe_dispatch
  *   and moe_forward_w4 skip.  Where the picked scores' sum is 0 the weights are 0 (scores are
- *   float32: one below 2^-126, of a softmax before its division, counts as 0).
+ *   float32: one below 2^-126, of a softmax before its division, counts as 0).  A score's relative
+ *   error is at most (1.2 |v| + 48) 2^-23, v the logit (sigmoid) or how far it lies below the row's
+ *   largest (softmax).
  *   topk_ids_dev int32 or int64 [num_tokens, top_k]; topk_weights_dev float32.
  *   Errors: MOE_ERR_INVALID_ARGUMENT (NULL, a bad enum, a stride below num_experts, groups
  *   that do not divide num_experts, top_groups outside [1, groups]), MOE_ERR_TOPK (top_k
@@ -175,10 +178,12 @@ int moe_prepare_weights_w4(const moe_w4_geom *g, const uint8_t *w1_codes_dev, co
  *     out[t] = sum over picks j of topk_weights[t, j] * W2_e (silu(Wg_e x[t]) * (Wu_e x[t]))
  *   The same function as moe_dispatch -> moe_expert_ffn -> moe_combine, for batches with few
  *   rows for each expert, whose time is that of reading the picked experts' weights.  Weights
- *   enter the products exactly (integers, scaled in float32) and so does x; the activation is
- *   rounded to the eleven bits of f16 (with a power of two for each 64 values of a row, so that
- *   its size does not matter); sums are float32; out is rounded once.  An infinity in a row of x
- *   makes the token's out not a number.
+ *   enter the products exactly (integers, scaled in float32), and so does x where the values of
+ *   each aligned run of 64 lie within 2^32 of each other (smaller ones to 2^-39 of the run's largest);
+ *   the activation is rounded to the eleven bits of f16 (with a power of two for each 64 values
+ *   of a row, so that its size does not matter), where moe_expert_ffn's default holds a pair of
+ *   bf16; sums are float32; out is rounded once.  An infinity in a row of x makes the token's
+ *   out not a number.
  *   x_dev, out_dev bf16 [num_tokens, hidden]; topk_ids_dev [num_tokens, top_k]: -1 is a masked
  *   pick, an id outside [-1, num_experts) is dropped and sets MOE_STATUS_BAD_EXPERT_ID.
  *   status_dev: one int32, written by the call (0: clean).  workspace_dev: 256-byte aligned.

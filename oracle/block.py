@@ -145,7 +145,10 @@ def unpack_w4(codes, scales):
 
 def forward_w4(x, ids, weights, w1, s1, w2, s2):
     """out [T, H] in float64, and the bound of a float32 evaluation that carries the activation
-    as a bf16 pair (2^-16) and rounds out to bf16 once."""
+    as a bf16 pair (2^-16) and rounds out to bf16 once: the arithmetic of the bf16 layer on the
+    weights that the codes stand for.  The 4-bit kernels carry the activation in f16 (2^-11), 32
+    times as coarse; they meet this narrower bound in the tests too, which only a sum whose
+    roundings all agreed would exceed."""
     T, H = x.shape
     I = w2.shape[2] * 2
     out, off = np.zeros((T, H)), np.zeros((T, H))
