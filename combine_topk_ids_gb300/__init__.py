@@ -13,10 +13,13 @@ bundles them with the buffers of one geometry.
 import ctypes
 import os
 
-from . import block
+from . import block, grouped
 from .block import (MoELayerW4, MoeNorm, MoeRouter, MoeW4Geom, make_router, make_w4_geom,  # noqa: F401
                     moe_add_rmsnorm, moe_add_rmsnorm_backward, moe_add_rmsnorm_workspace_size,
                     moe_forward_w4_workspace_size, moe_quantize_w4, moe_route_topk, moe_route_topk_backward)
+from .grouped import (MoeProduct, MoeQuantize, MoeRows, MoeSort, moe_product_fp8, moe_quantize_fp8,  # noqa: F401
+                      moe_sort_picks, moe_sort_picks_workspace_size, moe_sort_rows, moe_sort_rows_backward,
+                      moe_swiglu_fp8, moe_unsort_rows, moe_unsort_rows_backward)
 from .build import LIB_PATH, build  # noqa: F401
 
 LAYOUT = {"EM": 0, "RM": 1, "FLAT": 2}
@@ -98,6 +101,7 @@ def lib():
                   "moe_expert_ffn_fp8"):
             getattr(L, f).restype = ctypes.c_int
         block.bind(L)
+        grouped.bind(L)
         _lib = L
     return _lib
 
