@@ -349,7 +349,8 @@ def check_product(out, a, sa, b, sb, what="out"):
 
 PRODUCTS = [(1, 1, 128), (1, 4096, 7168), (2, 130, 256), (7, 1003, 1408), (12, 256, 512), (13, 384, 640), (16, 100, 2048),
             (25, 576, 1024), (33, 257, 896), (64, 128, 384), (65, 1000, 256), (128, 512, 4096), (129, 640, 1152),
-            (300, 1003, 1408), (777, 264, 128), (1500, 2000, 384), (2100, 2304, 512)]
+            (300, 1003, 1408), (777, 264, 128), (1500, 2000, 384), (2100, 2304, 512),
+            (3000, 1003, 384), (2999, 2308, 128), (1537, 4097, 640)]
 
 
 @pytest.mark.parametrize("M,N,K", PRODUCTS)
@@ -374,7 +375,8 @@ def test_product(M, N, K, dtype):
 
 
 GROUPED = [(3, 2, 8, 256, 128), (64, 8, 256, 128, 256), (40, 4, 16, 200, 384), (200, 4, 8, 384, 512), (300, 2, 4, 1003, 256),
-           (700, 2, 4, 640, 1024), (1300, 4, 8, 512, 384), (2500, 2, 3, 768, 256), (600, 8, 2, 257, 640)]
+           (700, 2, 4, 640, 1024), (1300, 4, 8, 512, 384), (2500, 2, 3, 768, 256), (600, 8, 2, 257, 640), (4000, 2, 4, 1003, 256),
+           (900, 8, 16, 1028, 640), (2100, 8, 3, 640, 128)]
 
 
 @pytest.mark.parametrize("T,k,E,N,K", GROUPED)
