@@ -23,21 +23,41 @@ struct QuantArgs {
     int row_blocks;           // BLOCK: blocks of 128 rows in a matrix
 };
 
-// 8 columns from p as floats.  EVEN: p is on a 16-byte boundary.
-template <typename T, bool EVEN>
-__device__ __forceinline__ void load8(const T *p, float (&f)[8]) {
-    if constexpr (EVEN && std::is_same_v<T, float>) {
-        const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
-        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w; f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-    } else if constexpr (EVEN) {
-        const uint4 v = *reinterpret_cast<const uint4 *>(p);
-        f[0] = lo_f32(v.x); f[1] = hi_f32(v.x); f[2] = lo_f32(v.y); f[3] = hi_f32(v.y);
-        f[4] = lo_f32(v.z); f[5] = hi_f32(v.z); f[6] = lo_f32(v.w); f[7] = hi_f32(v.w);
-    } else {
+// 8 columns as they lie in memory, and as floats.  EVEN: they start on a 16-byte boundary.
+template <typename T>
+struct Raw {
+    static constexpr int kVecs = sizeof(T) / 2;
+    uint4 v[kVecs];
+    template <bool EVEN> __device__ __forceinline__ void load(const T *p) {
+        if constexpr (EVEN) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = (float)p[j];
+            for (int i = 0; i < kVecs; ++i) v[i] = reinterpret_cast<const uint4 *>(p)[i];
+        } else if constexpr (sizeof(T) == 4) {
+            const uint32_t *w = reinterpret_cast<const uint32_t *>(p);
+            v[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            v[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        } else {
+            const uint16_t *w = reinterpret_cast<const uint16_t *>(p);
+            v[0] = make_uint4(w[0] | (uint32_t)w[1] << 16, w[2] | (uint32_t)w[3] << 16, w[4] | (uint32_t)w[5] << 16,
+                              w[6] | (uint32_t)w[7] << 16);
+        }
     }
-}
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) v[i] = make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void floats(float (&f)[8]) const {
+        if constexpr (sizeof(T) == 4) {
+            f[0] = __uint_as_float(v[0].x); f[1] = __uint_as_float(v[0].y);
+            f[2] = __uint_as_float(v[0].z); f[3] = __uint_as_float(v[0].w);
+            f[4] = __uint_as_float(v[1].x); f[5] = __uint_as_float(v[1].y);
+            f[6] = __uint_as_float(v[1].z); f[7] = __uint_as_float(v[1].w);
+        } else {
+            f[0] = lo_f32(v[0].x); f[1] = hi_f32(v[0].x); f[2] = lo_f32(v[0].y); f[3] = hi_f32(v[0].y);
+            f[4] = lo_f32(v[0].z); f[5] = hi_f32(v[0].z); f[6] = lo_f32(v[0].w); f[7] = hi_f32(v[0].w);
+        }
+    }
+};
 
 __device__ __forceinline__ float largest(const float (&f)[8]) {
     float m = 0.f;   // (fmaxf passes over what is not a number)
@@ -57,16 +77,18 @@ __device__ __forceinline__ uint2 codes8(const float (&f)[8], float inv) {
 
 // g / (1 + exp(-g)).  The exponential is the hardware's power of two of the rounded product
 // t = -g log2(e), times 1 + (what the rounding of t left out) ln 2: without that factor its error
-// would grow with |g|.  Where the power is 0 or infinite there is nothing to correct.
+// would grow with |g|.  t stops at 126, where silu is below 2^-119: the power stays finite, and its
+// reciprocal a normal number (the hardware's forms that handle others take several instructions each;
+// with them 32768 x 2048 takes 87 us).  An infinite g has no remainder: the maximum drops the NaN.
 __device__ __forceinline__ float silu(float g) {
     constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
     constexpr float kLog2eRest = 1.4426950408889634 - (double)kLog2e;   // of the constant's own rounding
     const float t = -g * kLog2e;
     float e, r;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(t));
-    const float rest = fmaf(-g, kLog2e, -t) - g * kLog2eRest;
-    if (fabsf(t) < 127.f) e = fmaf(e, rest * kLn2, e);
-    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fminf(t, 126.f)));
+    const float rest = fmaxf(fmaf(-g, kLog2eRest, fmaf(-g, kLog2e, -t)), -1.f);
+    e = fmaf(e, rest * kLn2, e);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
     return g * r;
 }
 
@@ -82,54 +104,61 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(QuantArgs 
     if (row >= a.R || (a.live && row >= *a.live)) return;
     const int c0 = ((int)(i - row * a.piece) * 32 * kQuantUnits + (threadIdx.x & 31)) * 8;
     const T *x = static_cast<const T *>(a.x) + row * a.stride;
-    float f[kQuantUnits][8], up[SWIGLU ? kQuantUnits : 1][8];
+    Raw<T> raw[kQuantUnits], raw_up[SWIGLU ? kQuantUnits : 1];
 #pragma unroll
     for (int u = 0; u < kQuantUnits; ++u) {
         const int c = c0 + 256 * u;
         if (c < a.cols) {
-            load8<T, EVEN>(x + c, f[u]);
-            if (SWIGLU) load8<T, EVEN>(x + a.cols + c, up[SWIGLU ? u : 0]);
+            raw[u].template load<EVEN>(x + c);
+            if (SWIGLU) raw_up[SWIGLU ? u : 0].template load<EVEN>(x + a.cols + c);
         } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[u][j] = up[SWIGLU ? u : 0][j] = 0.f;
+            raw[u].zero();
+            raw_up[SWIGLU ? u : 0].zero();
         }
     }
 #pragma unroll
     for (int u = 0; u < kQuantUnits; ++u) {
         const int c = c0 + 256 * u;
-        if (SWIGLU)
+        float f[8];
+        raw[u].floats(f);
+        if (SWIGLU) {
+            float up[8];
+            raw_up[SWIGLU ? u : 0].floats(up);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) f[u][j] = silu(f[u][j]) * up[SWIGLU ? u : 0][j];
-        float m = largest(f[u]);
+            for (int j = 0; j < 8; ++j) f[j] = silu(f[j]) * up[j];
+        }
+        float m = largest(f);
 #pragma unroll
         for (int o = 8; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAllLanes, m, o));
         m = fmaxf(m, 0x1p-100f);
         if (c >= a.cols) continue;
-        *reinterpret_cast<uint2 *>(a.codes + row * a.cols + c) = codes8(f[u], __fdiv_rn(448.f, m));
+        *reinterpret_cast<uint2 *>(a.codes + row * a.cols + c) = codes8(f, __fdiv_rn(448.f, m));
         if ((c & 127) == 0) a.scales[row * (a.cols >> 7) + (c >> 7)] = __fdiv_rn(m, 448.f);
     }
 }
 
 // A block takes 128 rows of 128 columns: 16 threads to a row, 16 rows at a time.
 template <typename T, bool EVEN>
-__global__ void __launch_bounds__(256) quantize_blocks_kernel(QuantArgs a) {
+__global__ void __launch_bounds__(256, 4) quantize_blocks_kernel(QuantArgs a) {
     __shared__ float red[8];
     pdl_wait();
     const int cb = a.cols >> 7;
     const int64_t i = blockIdx.x, block = i / cb, matrix = block / a.row_blocks;
     const int b = (int)(i - block * cb), r0 = (int)(block - matrix * a.row_blocks) * 128 + (threadIdx.x >> 4);
     const int c = b * 128 + (threadIdx.x & 15) * 8;
-    float f[8][8], m = 0.f;
+    Raw<T> raw[8];
+    float f[8], m = 0.f;
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
         if (r0 + 16 * u < a.rows)
-            load8<T, EVEN>(static_cast<const T *>(a.x) + (matrix * a.rows + r0 + 16 * u) * a.stride + c, f[u]);
-        else
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[u][j] = 0.f;
+            raw[u].template load<EVEN>(static_cast<const T *>(a.x) + (matrix * a.rows + r0 + 16 * u) * a.stride + c);
+        else raw[u].zero();
     }
 #pragma unroll
-    for (int u = 0; u < 8; ++u) m = fmaxf(m, largest(f[u]));
+    for (int u = 0; u < 8; ++u) {
+        raw[u].floats(f);
+        m = fmaxf(m, largest(f));
+    }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAllLanes, m, o));
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
@@ -139,9 +168,11 @@ __global__ void __launch_bounds__(256) quantize_blocks_kernel(QuantArgs a) {
     m = fmaxf(m, 0x1p-100f);
     const float inv = __fdiv_rn(448.f, m);
 #pragma unroll
-    for (int u = 0; u < 8; ++u)
+    for (int u = 0; u < 8; ++u) {
+        raw[u].floats(f);
         if (r0 + 16 * u < a.rows)
-            *reinterpret_cast<uint2 *>(a.codes + (matrix * a.rows + r0 + 16 * u) * a.cols + c) = codes8(f[u], inv);
+            *reinterpret_cast<uint2 *>(a.codes + (matrix * a.rows + r0 + 16 * u) * a.cols + c) = codes8(f, inv);
+    }
     if (threadIdx.x == 0) a.scales[block * cb + b] = __fdiv_rn(m, 448.f);
 }
 

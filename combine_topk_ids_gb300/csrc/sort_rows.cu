@@ -219,25 +219,26 @@ struct CopyArgs {
 };
 
 constexpr int kRowThreads = 256, kRowWarps = kRowThreads / 32;
-constexpr int kCopyWords = 4;   // accesses of a lane in a piece
+template <typename W> constexpr int kCopyWords = sizeof(W) == 16 ? 4 : 8;   // accesses of a lane in a piece
 
 // A warp copies one piece of a token's row (or of its scales) to the rows of its picks.
 template <typename W>
 __device__ __forceinline__ void copy_piece(const CopyArgs &a, const W *src, char *dst, int64_t stride, int words,
                                            int piece, int64_t t) {
-    const int lane = threadIdx.x & 31, c0 = piece * 32 * kCopyWords + lane;
+    constexpr int U = kCopyWords<W>;
+    const int lane = threadIdx.x & 31, c0 = piece * 32 * U + lane;
     const int32_t *pos = a.position + t * a.k;
     const int mine = lane < a.k ? pos[lane] : -1;
-    W v[kCopyWords];
+    W v[U];
 #pragma unroll
-    for (int u = 0; u < kCopyWords; ++u)
+    for (int u = 0; u < U; ++u)
         if (c0 + 32 * u < words) v[u] = src[c0 + 32 * u];
     for (int j = 0; j < a.k; ++j) {
         const int p = __shfl_sync(kAllLanes, mine, j);
         if (p < 0 || p >= a.num_rows) continue;
         W *d = reinterpret_cast<W *>(dst + p * stride);
 #pragma unroll
-        for (int u = 0; u < kCopyWords; ++u)
+        for (int u = 0; u < U; ++u)
             if (c0 + 32 * u < words) d[c0 + 32 * u] = v[u];
     }
 }
@@ -267,7 +268,7 @@ struct SumArgs {
 
 constexpr int kSumPicks = 4;    // picks whose loads are under way together
 
-template <int N> constexpr int kSumUnits = N == 1 ? 4 : 2;
+template <int N> constexpr int kSumUnits = N == 1 ? 8 : 2;
 
 // A warp sums one piece of a token's row over its picks, in their order.
 template <typename R, typename O, int N>
@@ -316,8 +317,10 @@ __global__ void __launch_bounds__(kRowThreads) unsort_rows_kernel(SumArgs a) {
     }
     O *out = static_cast<O *>(a.out) + t * a.ostride;
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-        if (c0 + 32 * N * u < a.H) Pack<O, N>::store(out + c0 + 32 * N * u, acc[u]);
+    for (int u = 0; u < U; ++u) {
+        const int c = c0 + 32 * N * u;
+        if (c < a.H) Pack<O, N>::store(out + c, acc[u]);
+    }
 }
 
 struct BackArgs {
@@ -330,12 +333,13 @@ struct BackArgs {
     int T, k, H, num_rows;
 };
 
-constexpr int kBackPicks = 8;   // picks that share a reading of dout
+template <int N> constexpr int kBackUnits = N == 1 ? 4 : 1;   // accesses of a thread and row under way
 
-// blockDim.x threads to a token, blockDim.y tokens to a block.
-template <typename R, typename O, int N>
+// blockDim.x threads to a token, blockDim.y tokens to a block; P picks share a reading of dout.
+template <typename R, typename O, int N, int P>
 __global__ void __launch_bounds__(256) unsort_rows_backward_kernel(BackArgs a) {
-    __shared__ float red[8][kBackPicks];
+    constexpr int U = kBackUnits<N>;
+    __shared__ float red[8][P];
     pdl_wait();
     const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     const bool live = t < a.T;
@@ -344,51 +348,72 @@ __global__ void __launch_bounds__(256) unsort_rows_backward_kernel(BackArgs a) {
     R *drows = static_cast<R *>(a.drows);
     const int nw = blockDim.x >> 5, lane = threadIdx.x & 31;
     const int warp = threadIdx.y * nw + (threadIdx.x >> 5);
-    for (int j0 = 0; j0 < a.k; j0 += kBackPicks) {
-        int p[kBackPicks];
-        float w[kBackPicks], dot[kBackPicks];
+    for (int j0 = 0; j0 < a.k; j0 += P) {
+        int p[P];
+        float w[P], dot[P];
 #pragma unroll
-        for (int q = 0; q < kBackPicks; ++q) {
+        for (int q = 0; q < P; ++q) {
             p[q] = live && j0 + q < a.k ? a.position[t * a.k + j0 + q] : -1;
             if (p[q] >= a.num_rows) p[q] = -1;
             w[q] = p[q] >= 0 && a.w ? a.w[t * a.k + j0 + q] : 1.f;
             dot[q] = 0.f;
         }
-        for (int c = threadIdx.x * N; live && c < a.H; c += blockDim.x * N) {
-            Pack<O, N> d;
-            d.load(dout + c);
-            Pack<R, N> v[kBackPicks];
+        for (int c0 = threadIdx.x * N; live && c0 < a.H; c0 += blockDim.x * N * U) {
+            Pack<O, N> d[U];
+            Pack<R, N> v[P][U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int c = c0 + u * blockDim.x * N;
+                if (c < a.H) d[u].load(dout + c);
+            }
             if (a.dw) {
 #pragma unroll
-                for (int q = 0; q < kBackPicks; ++q)
-                    if (p[q] >= 0) v[q].load(rows + p[q] * a.rstride + c);
+                for (int q = 0; q < P; ++q)
+                    if (p[q] >= 0)
+#pragma unroll
+                        for (int u = 0; u < U; ++u) {
+                            const int c = c0 + u * blockDim.x * N;
+                            if (c < a.H) v[q][u].load(rows + p[q] * a.rstride + c);
+                        }
             }
             if (a.drows) {
 #pragma unroll
-                for (int q = 0; q < kBackPicks; ++q)
-                    if (p[q] >= 0) {
-                        float g[N];
+                for (int q = 0; q < P; ++q)
+                    if (p[q] >= 0)
 #pragma unroll
-                        for (int n = 0; n < N; ++n) g[n] = w[q] * d.at(n);
-                        Pack<R, N>::store(drows + p[q] * a.dstride + c, g);
-                    }
+                        for (int u = 0; u < U; ++u) {
+                            const int c = c0 + u * blockDim.x * N;
+                            float g[N];
+#pragma unroll
+                            for (int n = 0; n < N; ++n) g[n] = w[q] * d[u].at(n);
+                            if (c < a.H) Pack<R, N>::store(drows + p[q] * a.dstride + c, g);
+                        }
             }
             if (a.dw) {
 #pragma unroll
-                for (int q = 0; q < kBackPicks; ++q)
+                for (int q = 0; q < P; ++q)
                     if (p[q] >= 0)
 #pragma unroll
-                        for (int n = 0; n < N; ++n) dot[q] = fmaf(d.at(n), v[q].at(n), dot[q]);
+                        for (int u = 0; u < U; ++u)
+                            if (c0 + u * blockDim.x * N < a.H)
+#pragma unroll
+                                for (int n = 0; n < N; ++n) dot[q] = fmaf(d[u].at(n), v[q][u].at(n), dot[q]);
             }
         }
         if (!a.dw) continue;
 #pragma unroll
-        for (int q = 0; q < kBackPicks; ++q) {
-            dot[q] = warp_sum(dot[q]);
-            if (lane == 0) red[warp][q] = dot[q];
+        for (int q = 0; q < P; ++q) dot[q] = warp_sum(dot[q]);
+        if (nw == 1) {
+#pragma unroll
+            for (int q = 0; q < P; ++q)
+                if (live && lane == q && j0 + q < a.k) a.dw[t * a.k + j0 + q] = dot[q];
+            continue;
         }
+        if (lane == 0)
+#pragma unroll
+            for (int q = 0; q < P; ++q) red[warp][q] = dot[q];
         __syncthreads();
-        if (live && (int)threadIdx.x < kBackPicks && j0 + (int)threadIdx.x < a.k) {
+        if (live && (int)threadIdx.x < P && j0 + (int)threadIdx.x < a.k) {
             float s = 0.f;
             for (int i = 0; i < nw; ++i) s += red[threadIdx.y * nw + i][threadIdx.x];
             a.dw[t * a.k + j0 + threadIdx.x] = s;
@@ -533,9 +558,9 @@ extern "C" int moe_sort_rows(const moe_rows *g, const void *x_dev, const float *
     const bool even = g->hidden * b % 16 == 0 && rows_on(x_dev, a.xstride, 1, 16) && rows_on(rows_dev, a.rstride, 1, 16);
     const int64_t word = even ? 16 : b;
     a.words = (int)(g->hidden * b / word);
-    constexpr int piece = 32 * kCopyWords;
+    const int piece = 32 * (word == 16 ? kCopyWords<uint4> : kCopyWords<uint32_t>);
     a.nchunk = (a.words + piece - 1) / piece;
-    a.nchunk_all = a.nchunk + (a.scales + piece - 1) / piece;
+    a.nchunk_all = a.nchunk + (a.scales + 32 * kCopyWords<float> - 1) / (32 * kCopyWords<float>);
     const int64_t blocks = blocks_of((int64_t)a.T * a.nchunk_all);
     if (blocks >= ((int64_t)1 << 31)) return MOE_ERR_LIMIT;
     auto launch = [&](auto w) {
@@ -593,11 +618,20 @@ extern "C" int moe_unsort_rows_backward(const moe_rows *g, const void *dout_dev,
                       rows_on(drows_dev, a.dstride, rb, n * rb);
     return with_row_types(g->rows_dtype, g->tokens_dtype, even, [&](auto r, auto o, auto width) {
         constexpr int N = decltype(width)::value;
-        const int64_t units = ((int64_t)a.H + N - 1) / N, turns = (units + 255) / 256;
-        const int threads = (int)(((units + turns - 1) / turns + 31) / 32 * 32);
-        const int tokens = 256 / threads;
+        // Threads for a token: all its accesses at once, up to a block, as long as the tokens alone are
+        // too few warps for the SMs; a warp to a token meets no barrier.
+        const int64_t turn = (int64_t)N * kBackUnits<N> * 32, most = ((int64_t)a.H + turn - 1) / turn;
+        const int64_t wanted = ((int64_t)num_sms() * 24 + a.T - 1) / a.T;
+        int warps = 1;
+        while (warps < 8 && warps < most && warps < wanted) warps *= 2;
+        const int tokens = 8 / warps;
         const int64_t blocks = ((int64_t)a.T + tokens - 1) / tokens;
-        return status_of(launch_pdl(unsort_rows_backward_kernel<decltype(r), decltype(o), N>, dim3((unsigned)blocks),
-                                    dim3(threads, tokens), 0, static_cast<cudaStream_t>(stream), a));
+        auto launch = [&](auto *kernel) {
+            return status_of(launch_pdl(kernel, dim3((unsigned)blocks), dim3(32 * warps, tokens), 0,
+                                        static_cast<cudaStream_t>(stream), a));
+        };
+        using R = decltype(r);
+        using O = decltype(o);
+        return a.k <= 4 ? launch(unsort_rows_backward_kernel<R, O, N, 4>) : launch(unsort_rows_backward_kernel<R, O, N, 8>);
     });
 }

@@ -73,7 +73,7 @@ typedef struct {
  *   moe_unsort_rows without weights.
  * moe_unsort_rows - out[t] = sum over j ascending of weights[t, j] * rows[position[t, j]], float32
  *   sums, rounded once; weights_dev float32 [num_tokens, top_k] or NULL (all 1).  A token without
- *   picks gets zeros.  A masked pick's weight is not read.
+ *   picks gets zeros.  A masked pick's weight does not matter.
  * moe_unsort_rows_backward - drows[position[t, j]] = weights[t, j] * dout[t] and
  *   dweights[t, j] = <dout[t], rows[position[t, j]]>, 0 for masked picks; drows (of rows_dtype,
  *   drows_stride) or dweights (float32 [num_tokens, top_k]) may be NULL, and so may rows without
