@@ -116,24 +116,34 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_rows_kernel(QuantArgs 
             raw_up[SWIGLU ? u : 0].zero();
         }
     }
+    float f[kQuantUnits][8], m[kQuantUnits];
 #pragma unroll
     for (int u = 0; u < kQuantUnits; ++u) {
-        const int c = c0 + 256 * u;
-        float f[8];
-        raw[u].floats(f);
+        raw[u].floats(f[u]);
         if (SWIGLU) {
             float up[8];
             raw_up[SWIGLU ? u : 0].floats(up);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = silu(f[j]) * up[j];
+            for (int j = 0; j < 8; ++j) f[u][j] = silu(f[u][j]) * up[j];
         }
-        float m = largest(f);
+        m[u] = largest(f[u]);
 #pragma unroll
-        for (int o = 8; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAllLanes, m, o));
-        m = fmaxf(m, 0x1p-100f);
+        for (int o = 8; o >= 1; o >>= 1) m[u] = fmaxf(m[u], __shfl_xor_sync(kAllLanes, m[u], o));
+        m[u] = fmaxf(m[u], 0x1p-100f);
+    }
+    // The two blocks' four quotients by one division: lanes 0 and 1 of every 16 have the factors, 2 and
+    // 3 the scales.
+    static_assert(kQuantUnits == 2, "four quotients");
+    const int lane = threadIdx.x & 15;
+    const float mine = lane & 1 ? m[1] : m[0];
+    const float q = __fdiv_rn(lane & 2 ? mine : 448.f, lane & 2 ? 448.f : mine);
+#pragma unroll
+    for (int u = 0; u < kQuantUnits; ++u) {
+        const int c = c0 + 256 * u;
+        const float inv = __shfl_sync(kAllLanes, q, u, 16);
         if (c >= a.cols) continue;
-        *reinterpret_cast<uint2 *>(a.codes + row * a.cols + c) = codes8(f, __fdiv_rn(448.f, m));
-        if ((c & 127) == 0) a.scales[row * (a.cols >> 7) + (c >> 7)] = __fdiv_rn(m, 448.f);
+        *reinterpret_cast<uint2 *>(a.codes + row * a.cols + c) = codes8(f[u], inv);
+        if (lane == 2 + u) a.scales[row * (a.cols >> 7) + (c >> 7)] = q;
     }
 }
 
