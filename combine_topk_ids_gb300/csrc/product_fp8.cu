@@ -3,6 +3,13 @@
 //
 //     out[m, n] = sum over blocks b of  sa[m, b] * sb[g, n / 128, b] * (a[m, b] . b[g, n, b])
 //
+// Bounds.  Few rows: the weights' bytes (HBM; 512 rows over 256 matrices of 4096 x 7168 786 us, 1.01 of
+// the measured copy rate), below some 50 MB of them the launch and the latency of one short wave of tiles (one
+// row by 4096 x 7168 7.9 us, 4.3 of them the bytes).  Many rows: the promotion, and close behind it the
+// operands' way into the ring (32768 x 4096 x 7168 692 us, 2.8 PFLOP/s; the products alone 424 us, with
+// their operands 592, with the promotion and no operands 640; the tensor cores are busy in half of the
+// cycles).
+//
 // A block of 128 inner columns is one k-step of the tensor cores: its sum (four K = 32 products of
 // tcgen05.mma kind::f8f6f4, exact products added in float32 in tensor memory) is scaled as a whole
 // and added to float32 registers, the "promotion" of the partial sum.
@@ -12,7 +19,9 @@
 // has one output column, a register one row.  192 threads:
 //   warp 0      fills a ring of stages (128 x 128 weights, NT x 128 rows) with TMA
 //   warp 1      issues the products, each k-step into the next of several buffers in tensor memory
-//   warps 2-5   promotion; the scales' products of the next eight k-steps lie in shared memory
+//   warps 2-5   promotion
+//   warp 7      puts the scales' products of the next eight k-steps into shared memory: a promoting warp
+//               that had loads of its own under way would wait for them with its tensor-memory loads
 // Where the tiles are fewer than the SMs, `split` blocks of a cluster share a tile's k-steps and add
 // their sums up through distributed shared memory, in the blocks' order.
 #include <cuda_bf16.h>
@@ -26,7 +35,7 @@ namespace {
 
 constexpr int kBK = 128;            // inner columns (bytes) of a k-step
 constexpr int kTileN = 128;         // output columns of a tile: one block of the weights' scales
-constexpr int kThreads = 224;
+constexpr int kThreads = 256;
 constexpr int kScaleSteps = 8;      // k-steps of one table of scales
 constexpr int kMaxSplit = 8;        // blocks that share a tile (what any GPU's clusters hold)
 
@@ -222,15 +231,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     float *table = reinterpret_cast<float *>(smem + S::kStages * S::kStage);   // [2][kScaleSteps][NT]
     uint64_t *bars = reinterpret_cast<uint64_t *>(reinterpret_cast<uint8_t *>(table) + 2 * S::kTable);
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * S::kStages + 2 * S::kBuffers);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2 * S::kStages + 2 * S::kBuffers + 4);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int32_t *no_status = reinterpret_cast<int32_t *>(tmem_slot + 2);
-    int *wsum = reinterpret_cast<int *>(tmem_slot + 3);                        // [7]
-    Tile *mine_s = reinterpret_cast<Tile *>(wsum + 7);
+    int *wsum = reinterpret_cast<int *>(tmem_slot + 3);                        // [8]
+    Tile *mine_s = reinterpret_cast<Tile *>(wsum + 8);
     int *prefix = reinterpret_cast<int *>(bars) + 512 / 4;                     // [G + 1]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * S::kStages;
     const uint32_t pfull0 = empty0 + 8 * S::kStages, pempty0 = pfull0 + 8 * S::kBuffers;
+    const uint32_t sfull0 = pempty0 + 8 * S::kBuffers, sempty0 = sfull0 + 16;
     int32_t *status = a.status ? a.status : no_status;
 
     if (threadIdx.x == 0) {
@@ -241,6 +251,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int b = 0; b < S::kBuffers; ++b) {
             mbar_init(pfull0 + 8 * b, 1);
             mbar_init(pempty0 + 8 * b, 4);   // one arrival of each promoting warp
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(sfull0 + 8 * b, 1);
+            mbar_init(sempty0 + 8 * b, 4);
         }
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -305,41 +319,44 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if ((buf += 2) >= S::kBuffers) { buf = odd; bphase ^= 1; }
             }
         }
-    } else {
-        const int thread = threadIdx.x - 64, quad = warp & 3, col = quad * 32 + lane;
-        const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-        int buf = 0, turn = 0;
-        uint32_t bphase = 0;
+    } else if (warp == 7) {
+        // lane: k-step lane % 8, rows lane / 8 and every fourth behind it; what is fetched waits in registers
+        // for its table to be free
+        uint32_t turn = 0;
         bool ok = true;
-        // (Where a wait has given up the loops go on to their end without waiting: the four warps
-        // meet at the tables' barriers as often as ever.)
-        for (int i = first; i < total; i += step) {
+        for (int i = first; i < total && ok; i += step) {
+            const Tile t = tile_of<NT>(a, prefix, i);
+            const float *sa = a.sa + (int64_t)(t.m0 + (lane >> 3)) * a.kb + (lane & 7);
+            const float *sb = a.sb + ((int64_t)t.g * a.nblk + t.nb) * a.kb + (lane & 7);
+            for (int k = k0; k < k1; k += kScaleSteps, ++turn) {
+                float *tab = table + (turn & 1) * (kScaleSteps * NT);   // [8][NT]
+                const bool in = k + (lane & 7) < k1;
+                const float w = in ? __ldg(sb + k) : 0.f;
+                float r[NT / 4];
+#pragma unroll
+                for (int j = 0; j < NT / 4; ++j)
+                    r[j] = in && 4 * j + (lane >> 3) < t.rows ? __ldg(sa + (int64_t)(4 * j) * a.kb + k) : 0.f;
+                if (!mbar_wait(sempty0 + 8 * (turn & 1), ((turn >> 1) & 1) ^ 1, abort_flag, status)) { ok = false; break; }
+#pragma unroll
+                for (int j = 0; j < NT / 4; ++j) tab[(lane & 7) * NT + 4 * j + (lane >> 3)] = w * r[j];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sfull0 + 8 * (turn & 1));
+            }
+        }
+    } else {
+        const int quad = warp & 3, col = quad * 32 + lane;
+        const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+        int buf = 0;
+        uint32_t bphase = 0, turn = 0;
+        bool ok = true;
+        for (int i = first; i < total && ok; i += step) {
             const Tile t = tile_of<NT>(a, prefix, i);
             mine = t;
 #pragma unroll
             for (int c = 0; c < NT / 2; ++c) acc[c] = make_float2(0.f, 0.f);
-            // Scales of eight k-steps: thread -> row thread / 8 (and every 16th after it), k-step
-            // thread % 8.  Fetched while the eight before them are promoted.
-            constexpr int kEach = NT / 16;
-            float next[kEach];
-            const float *sb = a.sb + ((int64_t)t.g * a.nblk + t.nb) * a.kb;
-            auto fetch = [&](int k) {
-                k += thread & 7;
-                const float b = k < k1 ? __ldg(sb + k) : 0.f;
-#pragma unroll
-                for (int r = 0; r < kEach; ++r) {
-                    const int row = (thread >> 3) + 16 * r;
-                    next[r] = k < k1 && row < t.rows ? b * __ldg(a.sa + (int64_t)(t.m0 + row) * a.kb + k) : 0.f;
-                }
-            };
-            fetch(k0);
-            for (int k = k0; k < k1; k += kScaleSteps) {
-                float *tab = table + turn * (kScaleSteps * NT);
-                turn ^= 1;   // (two tables: all warps are past the one before the last barrier)
-#pragma unroll
-                for (int r = 0; r < kEach; ++r) tab[(thread & 7) * NT + (thread >> 3) + 16 * r] = next[r];
-                asm volatile("bar.sync 1, 128;" ::: "memory");
-                fetch(k + kScaleSteps);
+            for (int k = k0; k < k1 && ok; k += kScaleSteps, ++turn) {
+                const float *tab = table + (turn & 1) * (kScaleSteps * NT);
+                if (!mbar_wait(sfull0 + 8 * (turn & 1), (turn >> 1) & 1, abort_flag, status)) { ok = false; break; }
                 const int n = min(kScaleSteps, k1 - k);
                 for (int q = 0; q < n && ok; ++q) {
                     if (!mbar_wait(pfull0 + 8 * buf, bphase, abort_flag, status)) { ok = false; break; }
@@ -368,6 +385,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (++buf == S::kBuffers) { buf = 0; bphase ^= 1; }
                 }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sempty0 + 8 * (turn & 1));
             }
             const int n = t.nb * kTileN + col;
             if (a.split == 1 && n < a.N && ok) {
@@ -451,7 +470,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 //                loads of its own under way would wait for them with its tensor-memory loads
 //   warps 4-11   promotion: warp % 4 gives the rows, warps 4-7 and 8-11 the two blocks of 128 columns
 // A k-step's 128 x 256 sums take half of the tensor memory; the products fill one half while the other
-// is promoted.
+// is promoted.  The promotion has 256 cycles of additions for the 512 of the products, and as many of
+// loads; what it loses it loses between them: what a warp does besides them lies behind a load that is
+// under way (776 us where the scales' part lay in front of it).
 constexpr int kWideThreads = 384;
 constexpr int kWideN = 256;
 constexpr int kWideLaunchRegs = 168, kWideControlRegs = 72, kWidePromoteRegs = 216;
@@ -640,44 +661,44 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             float2 acc[64];
 #pragma unroll
             for (int c = 0; c < 64; ++c) acc[c] = make_float2(0.f, 0.f);
-#pragma unroll 1
-            for (int k0 = 0; k0 < a.kb && ok; k0 += 4) {
-                const float s[4] = {sa.x * sb.x, sa.y * sb.y, sa.z * sb.z, sa.w * sb.w};
-                if (k0 & 4 || k0 + 4 >= a.kb) {       // the table's last four
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(sempty0 + 8 * (turn & 1));
-                    ++turn;
-                    if (k0 + 4 < a.kb || i + step < total)
-                        if (!mbar_wait(sfull0 + 8 * (turn & 1), (turn >> 1) & 1, abort_flag, status)) { ok = false; break; }
-                    scales(0);                        // (behind the last of all: not used)
-                } else scales(1);
-#pragma unroll 1
-                for (int q = 0; q < 4; ++q) {
-                    if (k0 + q >= a.kb) break;
-                    const float c = q < 2 ? (q ? s[1] : s[0]) : q == 2 ? s[2] : s[3];
-                    const uint32_t buf = it & 1, from = tmem_base + buf * kWideN + lanes;
-                    if (!mbar_wait(pfull0 + 8 * buf, (it >> 1) & 1, abort_flag, status)) { ok = false; break; }
-                    tc_fence_after();
-                    ++it;
-                    // the next 32 columns are on their way while 32 are added; the buffer is free as
-                    // soon as the last are in registers
-                    uint32_t u[32], v[32];
-                    tmem_ld32(from, u);
-                    tmem_wait(u);
-                    tmem_ld32(from + 32, v);
-                    add32<0>(acc, u, c);
-                    tmem_wait(v);
-                    tmem_ld32(from + 64, u);
-                    add32<32>(acc, v, c);
-                    tmem_wait(u);
-                    tmem_ld32(from + 96, v);
-                    add32<64>(acc, u, c);
-                    tmem_wait(v);
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(pempty0 + 8 * buf);
-                    add32<96>(acc, v, c);
+            float s[4];
+#pragma unroll 4
+            for (int k = 0; k < a.kb; ++k) {
+                const uint32_t buf = it & 1, from = tmem_base + buf * kWideN + lanes;
+                if (!mbar_wait(pfull0 + 8 * buf, (it >> 1) & 1, abort_flag, status)) { ok = false; break; }
+                tc_fence_after();
+                ++it;
+                // the next 32 columns are on their way while 32 are added; the buffer is free as soon as
+                // the last are in registers
+                uint32_t u[32], v[32];
+                tmem_ld(from, u);
+                const int q = k & 3;
+                if (q == 0) {
+                    s[0] = sa.x * sb.x; s[1] = sa.y * sb.y; s[2] = sa.z * sb.z; s[3] = sa.w * sb.w;
+                    if (k & 4 || k + 4 >= a.kb) {     // the table's last four
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(sempty0 + 8 * (turn & 1));
+                        ++turn;
+                        if (k + 4 < a.kb || i + step < total)
+                            if (!mbar_wait(sfull0 + 8 * (turn & 1), (turn >> 1) & 1, abort_flag, status)) { ok = false; break; }
+                        scales(0);                    // (behind the last of all: not used)
+                    } else scales(1);
                 }
+                const float c = q < 2 ? (q ? s[1] : s[0]) : q == 2 ? s[2] : s[3];
+                tmem_wait(u);
+                tmem_ld(from + 32, v);
+                add32<0>(acc, u, c);
+                tmem_wait(v);
+                tmem_ld(from + 64, u);
+                add32<32>(acc, v, c);
+                tmem_wait(u);
+                tmem_ld(from + 96, v);
+                add32<64>(acc, u, c);
+                tmem_wait(v);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(pempty0 + 8 * buf);
+                add32<96>(acc, v, c);
             }
             if (!ok) break;
             const Tile done = t;
@@ -896,18 +917,19 @@ struct Choice {
 // what comes before and after them about 1 us (wide: 1.5), sharing a tile 1 to 2 us more (among 8 blocks
 // up to 3).  Several groups' weights come from HBM, 16 KB (wide: 32) for a k-step, and a group of r rows is taken for r / rows + 1/2 row tiles, as the rows of groups of different sizes come to.
 // Measured, us, by tiles of 16, 32, 64 and 128 rows and wide ones:
-//     rows x n x k             1 x 4096 x 7168    7.7   8.5  10.3  14.6   28.8
-//                             64 x 4096 x 7168   14.8  12.2  10.7  13.1   32.4
-//                            128 x 4096 x 7168   26.3  16.7  14.9  14.4   34.5
-//                            512 x 4096 x 7168   81.2  55.3  40.0  37.4   35.3
-//                            777 x 1003 x 1408   11.5  10.6   8.8  11.6   17.8
+//     rows x n x k             1 x 4096 x 7168    7.9   8.6  10.5  14.8   28.8
+//                             64 x 4096 x 7168   14.9  11.5  10.5  13.2   32.4
+//                            128 x 4096 x 7168   26.0  16.3  14.7  14.5   34.5
+//                            512 x 4096 x 7168   80.8  52.5  40.7  34.8   33.6
+//                            777 x 1003 x 1408   11.3  10.5   9.2  11.8   17.8
 //     256 groups, 8 rows each, 4096 x 7168        1068  1079  1093  1676   1146
 //                16 rows                          1145  1098  1106  1699   1156
 //                32 rows                          1594  1217  1172  1743   1175
 //                64 rows                             -     -  1474     -   1242
+// (the groups before the scales had a warp of their own, which brought 2 to 4% to all)
 Choice choose_tiles(const ProductArgs &p) {
     static const struct { int rows, n, step, around; } kTiles[] = {
-        {16, kTileN, 200, 1000}, {32, kTileN, 230, 1000}, {64, kTileN, 320, 1000}, {128, kTileN, 600, 1000}, {0, kWideN, 500, 1500}};
+        {16, kTileN, 200, 1000}, {32, kTileN, 230, 1000}, {64, kTileN, 320, 1000}, {128, kTileN, 550, 1000}, {0, kWideN, 500, 1500}};
     const int64_t sms = num_sms();
     Choice best{16, 1};
     int64_t least = INT64_MAX;

@@ -3,6 +3,10 @@
 // include/moe_grouped.h).
 //
 //     a = max(largest |v| of the block, 2^-100);  scale = a / 448;  code = e4m3(v * (448 / a))
+//
+// Each value is read once and held in registers between the maximum and the codes.  HBM bounds it: 32768 x
+// 7168 bf16 rows 114 us, 0.92 of the copy rate, as weights 116 us; SwiGLU of 32768 x 2048 58 us, 0.86, the
+// instructions close behind (the schedulers issue in 80% of the cycles).
 #include <cuda_fp8.h>
 
 #include <type_traits>

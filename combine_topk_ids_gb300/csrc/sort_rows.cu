@@ -4,6 +4,10 @@
 // Picks (t, j) are ordered by (expert, t, j).  A pick's row is
 //     the picks of smaller experts + the earlier picks of its own expert,
 // both counts, so no atomic decides a position.
+//
+// The rows' kernels read and write each row once; HBM bounds them where rows are on 16-byte boundaries
+// (measured, of the copy rate: 32768 tokens of 7168 bf16 columns, top-8, sorted 647 us, 0.97, and e4m3
+// with its order 346 us, 0.93; back 587 us; the gradient of 8192 of them 311 us, 0.95).
 #include "../../include/moe_grouped.h"
 #include "block_common.cuh"
 
@@ -48,6 +52,9 @@ __global__ void __launch_bounds__(512) sort_count_kernel(SortArgs a) {
     if (threadIdx.x == 0) a.hist[(int64_t)a.nb * a.E + blockIdx.x] = bad;
 }
 
+// Up to 4096 picks one block does it all (512 picks over 256 experts: 4 us of latency); above, every
+// block counts its picks first, and then reads the counts of all (262144 picks: 15 us in both kernels).
+//
 // Each warp owns a contiguous run of the block's picks: it counts the run by expert, the counts
 // become the first position of its run in each expert, and then it ranks the run 32 at a time.
 __global__ void __launch_bounds__(1024) sort_assign_kernel(SortArgs a) {
@@ -221,7 +228,8 @@ struct CopyArgs {
 constexpr int kRowThreads = 256, kRowWarps = kRowThreads / 32;
 template <typename W> constexpr int kCopyWords = sizeof(W) == 16 ? 4 : 8;   // accesses of a lane in a piece
 
-// A warp copies one piece of a token's row (or of its scales) to the rows of its picks.
+// A warp copies one piece of a token's row (or of its scales) to the rows of its picks: the row is read
+// once, and a lane's four stores of a pick do not wait for one another.
 template <typename W>
 __device__ __forceinline__ void copy_piece(const CopyArgs &a, const W *src, char *dst, int64_t stride, int words,
                                            int piece, int64_t t) {
@@ -270,7 +278,10 @@ constexpr int kSumPicks = 4;    // picks whose loads are under way together
 
 template <int N> constexpr int kSumUnits = N == 1 ? 8 : 2;
 
-// A warp sums one piece of a token's row over its picks, in their order.
+// A warp sums one piece of a token's row over its picks, in their order.  Rows off 16-byte boundaries go
+// column by column, eight of a lane under way for each of four picks (16381 x 2047 bf16, top-4, 76 us,
+// 0.66 of the copy rate; four columns 85).  Pairs of bf16 were slower: 142 us as words or halves by
+// address, 105 as aligned words and a shuffle.
 template <typename R, typename O, int N>
 __global__ void __launch_bounds__(kRowThreads) unsort_rows_kernel(SumArgs a) {
     constexpr int U = kSumUnits<N>;
@@ -335,7 +346,10 @@ struct BackArgs {
 
 template <int N> constexpr int kBackUnits = N == 1 ? 4 : 1;   // accesses of a thread and row under way
 
-// blockDim.x threads to a token, blockDim.y tokens to a block; P picks share a reading of dout.
+// blockDim.x threads to a token, blockDim.y tokens to a block; P picks share a reading of dout.  A warp to
+// a token where there are tokens enough: 16381 x 2048 bf16, top-4, 86 us (0.95 of the copy rate; a block to
+// a token 168).  Rows off 16-byte boundaries column by column, four of a lane under way for each pick
+// (x 2047 160 us, 0.5: the schedulers issue in 67% of the cycles; one column 186, eight 203).
 template <typename R, typename O, int N, int P>
 __global__ void __launch_bounds__(256) unsort_rows_backward_kernel(BackArgs a) {
     constexpr int U = kBackUnits<N>;
