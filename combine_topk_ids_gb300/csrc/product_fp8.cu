@@ -48,6 +48,7 @@ struct ProductArgs {
     int M, N, kb;               // kb: k-steps
     int G, nblk;                // weight matrices (1 without offsets), tiles across the columns
     int split;                  // blocks of a cluster that share a tile
+    int most_rows;              // row tiles there can be
     int panel;                  // wide tiles: tiles across the columns of a panel
     int out_bf16;
     int out_fours;              // four neighbouring columns of out can be stored at once
@@ -60,39 +61,43 @@ __device__ __forceinline__ int row_of(const ProductArgs &a, int g) {
     return min(max(__ldg(a.offsets + g), 0), a.M);
 }
 
-// prefix[g] = tiles of `rows` rows in the groups before g, g <= G.  All threads of the block.
-__device__ __forceinline__ void count_tiles(const ProductArgs &a, int rows, int *prefix, int *wsum) {
+// prefix[g] = tiles of `rows` rows in the groups before g, g <= G; the number of tiles.  All threads of the
+// block.  Sums stop at 2^30 - 1, above what ascending offsets can come to (most_rows): offsets that do not
+// ascend and pass it get no tile.
+__device__ __forceinline__ int count_tiles(const ProductArgs &a, int rows, int *prefix, int *wsum) {
+    constexpr int kStop = (1 << 30) - 1;
     if (!a.offsets) {
         if (threadIdx.x == 0) {
             prefix[0] = 0;
-            prefix[1] = (a.M + rows - 1) / rows;
+            prefix[1] = a.most_rows;
         }
         __syncthreads();
-        return;
+        return a.most_rows * a.nblk;
     }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     int carry = 0;
     for (int g0 = 0; g0 < a.G; g0 += blockDim.x) {
         const int g = g0 + threadIdx.x;
-        const int n = g < a.G ? (max(row_of(a, g + 1) - row_of(a, g), 0) + rows - 1) / rows : 0;
+        const int n = g < a.G ? (int)(((int64_t)max(row_of(a, g + 1) - row_of(a, g), 0) + rows - 1) / rows) : 0;
         int incl = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int v = __shfl_up_sync(kAllLanes, incl, o);
-            if (lane >= o) incl += v;
+            if (lane >= o) incl = min(incl + v, kStop);
         }
         if (lane == 31) wsum[warp] = incl;
         __syncthreads();
         int ahead = carry;
         for (int w = 0; w < warps; ++w) {
-            ahead += w < warp ? wsum[w] : 0;
-            carry += wsum[w];
+            if (w < warp) ahead = min(ahead + wsum[w], kStop);
+            carry = min(carry + wsum[w], kStop);
         }
-        if (g < a.G) prefix[g] = ahead + incl - n;
+        if (g < a.G) prefix[g] = min(ahead + incl, kStop) - n;
         __syncthreads();
     }
     if (threadIdx.x == 0) prefix[a.G] = carry;
     __syncthreads();
+    return carry <= a.most_rows ? carry * a.nblk : 0;
 }
 
 struct Tile {
@@ -272,8 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     pdl_wait();
-    count_tiles(a, NT, prefix, wsum);
-    const int total = prefix[a.G] * a.nblk;
+    const int total = count_tiles(a, NT, prefix, wsum);
     // the k-steps of this block, and its cluster's tiles
     const int rank = a.split > 1 ? (int)cluster_rank() : 0;
     const int k0 = (int)((int64_t)a.kb * rank / a.split), k1 = (int)((int64_t)a.kb * (rank + 1) / a.split);
@@ -488,7 +492,8 @@ struct Wide {
     static constexpr int kOut = 32 * 256;                             // a warp's way out: 32 rows of 256 bytes
     // scales of eight k-steps: one to a row, and one to each half of the columns; two such tables
     static constexpr int kTable = (128 + 2) * kScaleSteps * 4;
-    static constexpr int kBytes = 1024 + kStages * kStage + 8 * kOut + 2 * kTable + 256;
+    static constexpr int kTiles = 8;   // tiles whose place the producer has told the promoting warps (it is six ahead at most)
+    static constexpr int kBytes = 1024 + kStages * kStage + 8 * kOut + 2 * kTable + 512;
 };
 
 // acc (columns 2i and 2i + 1 of BASE + ..) += c * v
@@ -533,7 +538,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int32_t *no_status = reinterpret_cast<int32_t *>(tmem_slot + 2);
     int *wsum = reinterpret_cast<int *>(tmem_slot + 3);                    // [12]
-    int *prefix = reinterpret_cast<int *>(bars) + 256 / 4;                 // [G + 1]
+    Tile *tiles = reinterpret_cast<Tile *>(wsum + 12);                     // [kTiles]
+    int *prefix = reinterpret_cast<int *>(bars) + 512 / 4;                 // [G + 1]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * S::kFull;
     const uint32_t pfull0 = empty0 + 8 * S::kStages, pempty0 = pfull0 + 16, sfull0 = pfull0 + 32, sempty0 = pfull0 + 48;
@@ -562,18 +568,20 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     pdl_wait();
-    count_tiles(a, S::kRows, prefix, wsum);
-    const int total = prefix[a.G] * a.nblk;
+    const int total = count_tiles(a, S::kRows, prefix, wsum);
     const int first = blockIdx.x, step = gridDim.x;
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWideControlRegs));
         if (warp == 0 && lane == 0) {
             int stage = 0, place = 0;
-            uint32_t phase = 0;
+            uint32_t phase = 0, nth = 0;
             bool ok = true;
             for (int i = first; i < total && ok; i += step) {
-                const Tile t = wide_tile(a, prefix, i);
+                // (the promoting warps see it with the sums of the tile's first k-step; they are done with
+                // the tile eight before: its sums are out of the tensor memory, and the ring and that hold
+                // five k-steps)
+                const Tile t = tiles[nth++ % S::kTiles] = wide_tile(a, prefix, i);
                 for (int k = 0; k < a.kb; ++k) {
                     if (!mbar_wait(empty0 + 8 * stage, phase ^ 1, abort_flag, status)) { ok = false; break; }
                     const uint32_t fb = full0 + 8 * place, at = smem_u32(smem + stage * S::kStage);
@@ -655,14 +663,13 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         };
         bool ok = first >= total || mbar_wait(sfull0, 0, abort_flag, status);
         scales(0);
-        Tile t{};
-        if (first < total) t = wide_tile(a, prefix, first);
+        uint32_t nth = 0;
         for (int i = first; i < total; i += step) {
             float2 acc[64];
 #pragma unroll
             for (int c = 0; c < 64; ++c) acc[c] = make_float2(0.f, 0.f);
             float s[4];
-#pragma unroll 4
+#pragma unroll 8
             for (int k = 0; k < a.kb; ++k) {
                 const uint32_t buf = it & 1, from = tmem_base + buf * kWideN + lanes;
                 if (!mbar_wait(pfull0 + 8 * buf, (it >> 1) & 1, abort_flag, status)) { ok = false; break; }
@@ -701,8 +708,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 add32<96>(acc, v, c);
             }
             if (!ok) break;
-            const Tile done = t;
-            if (i + step < total) t = wide_tile(a, prefix, i + step);
+            const Tile done = tiles[nth++ % S::kTiles];
             // Out: the warp's 32 rows of 128 columns, 256 bytes of each row at a time through shared memory:
             // two boxes of 32 rows x 128 bytes, which leave as TMA stores where all rows count
             const int n0 = done.nb * kWideN + 128 * half, cols = min(128, a.N - n0);
@@ -737,7 +743,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 if (a.out_map && n * size % 16 == 0) {         // two rows at a time, 16 bytes to a lane
                     const int at = (lane & 15) * 16;
                     if (at < n * size)
-#pragma unroll 4
+#pragma unroll 8
                         for (int r = lane >> 4; r < valid; r += 2)
                             *reinterpret_cast<uint4 *>(to + r * a.out_stride * size + at) = *reinterpret_cast<const uint4 *>(
                                 way_out + (at >> 7) * 4096 + r * 128 + ((at & 127) ^ ((r & 7) << 4)));
@@ -856,7 +862,7 @@ struct Operands {
 };
 
 template <int NT>
-int launch_narrow(const ProductArgs &p, const Operands &o, cudaStream_t s) {
+int launch_narrow(ProductArgs p, const Operands &o, cudaStream_t s) {
     using S = Narrow<NT>;
     CUtensorMap rows, weights;
     if (!make_codes_map(&rows, o.a, p.M, o.K, o.a_stride, NT) ||
@@ -868,7 +874,8 @@ int launch_narrow(const ProductArgs &p, const Operands &o, cudaStream_t s) {
     const cudaError_t e = devices.set(kernel, S::kBytes + (MOE_MAX_EXPERTS + 1) * 4,
                                       [](int) { return cudaSuccess; });
     if (e != cudaSuccess) return status_of(e);
-    const int64_t most = most_tiles(p, NT) * p.nblk;
+    p.most_rows = (int)most_tiles(p, NT);
+    const int64_t most = (int64_t)p.most_rows * p.nblk;
     if (most >= ((int64_t)1 << 31)) return MOE_ERR_LIMIT;
     const int sms = num_sms();
     const int64_t grid = p.split > 1 ? most * p.split : (most < sms ? most : sms);
@@ -902,7 +909,8 @@ int launch_wide(ProductArgs p, const Operands &o, cudaStream_t s) {
     p.nblk = (p.N + kWideN - 1) / kWideN;
     const int64_t panel = ((int64_t)32 << 20) / (kWideN * o.K);
     p.panel = panel < 1 ? 1 : panel < p.nblk ? (int)panel : p.nblk;
-    const int64_t most = most_tiles(p, S::kRows) * p.nblk;
+    p.most_rows = (int)most_tiles(p, S::kRows);
+    const int64_t most = (int64_t)p.most_rows * p.nblk;
     if (most >= ((int64_t)1 << 31)) return MOE_ERR_LIMIT;
     const int64_t grid = most < num_sms() ? most : num_sms();
     return launch_clusters(kernel, grid, 1, kWideThreads, S::kBytes + (p.G + 1) * 4, s, rows, weights, out, p);
@@ -983,7 +991,7 @@ extern "C" int moe_product_fp8(const moe_product *p, const uint8_t *a_dev, const
     if (rc != MOE_OK) return rc;
     if (p->num_rows == 0) return MOE_OK;
     ProductArgs args{a_scales_dev, b_scales_dev, offsets_dev, out_dev, status_dev, out_stride, p->num_rows, p->n,
-                     p->k / kBK, p->groups ? p->groups : 1, (p->n + kTileN - 1) / kTileN, 1, 1,
+                     p->k / kBK, p->groups ? p->groups : 1, (p->n + kTileN - 1) / kTileN, 1, 0, 1,
                      p->out_dtype == MOE_DTYPE_BF16, 0, 0};
     const size_t four = 4 * dtype_bytes(p->out_dtype);
     args.out_fours = is_aligned(out_dev, four) && out_stride % 4 == 0;

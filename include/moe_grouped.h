@@ -137,8 +137,9 @@ typedef struct {
  *   a_dev        e4m3 [num_rows, k]; a_scales_dev float32 [num_rows, k / 128]
  *   b_dev        e4m3 [groups, n, k] (packed); b_scales_dev float32 [groups, ceil(n / 128), k / 128]
  *   offsets_dev  int32 [groups + 1]: group g has the rows [offsets[g], offsets[g + 1]), ascending, as
- *                moe_sort_picks writes them (values are taken as if clamped to [0, num_rows]); rows
- *                of no group are left as they were in out and do not matter in a
+ *                moe_sort_picks writes them (values are taken as if clamped to [0, num_rows]; where
+ *                they do not ascend, what out holds afterwards is undefined); rows of no group are left
+ *                as they were in out and do not matter in a
  *   out_dev      bf16 or float32 [num_rows, n]; does not overlap the inputs
  *   status_dev   one int32 into which MOE_STATUS_TIMEOUT is or-ed where a wait of the kernel gave
  *                up, or NULL; the caller clears it

@@ -417,6 +417,21 @@ def test_product_offsets_of_all_kinds():
                 check_product(out[c[e]:c[e + 1]], a[c[e]:c[e + 1]], sa[c[e]:c[e + 1]], b[e], sb[e])
 
 
+@pytest.mark.parametrize("M,N", [(70, 130), (900, 2100)])
+def test_product_offsets_that_do_not_ascend(M, N):
+    """Nothing beyond out is written, and the next call is right."""
+    K = 256
+    a, sa = codes_of(M, K, block=1, seed=1)
+    b, sb = codes_of(9, N, K, block=128, seed=2)
+    room = torch.full((3 * M, N), 7.0, device="cuda")
+    low, high = -(1 << 31), (1 << 31) - 1
+    for off in ([0, M, 0, M, 0, M, 0, M, 0, M], [high, low] * 5, [M, 9, M, 8, M, 7, M, 6, M, 5], [5, 0, 1, 0, 1, 0, 1, 0, 1, 0]):
+        moe.moe_product_fp8(a, sa, b, sb, room[M:2 * M], offsets=torch.tensor(off, dtype=I32, device="cuda"))
+        assert (room[:M] == 7).all() and (room[2 * M:] == 7).all()
+    moe.moe_product_fp8(a, sa, b[:1], sb[:1], room[M:2 * M], offsets=torch.tensor([0, M], dtype=I32, device="cuda"))
+    check_product(room[M:2 * M], a, sa, b[0], sb[0])
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 256, 1024), (200, 300, 512), (1600, 2100, 256)])
 def test_product_extremes(M, N, K):
     """Largest codes, scales at both ends of float32, NaN in one row and in one block of weights."""
