@@ -3,10 +3,10 @@
 //
 //     out[m, n] = sum over blocks b of  sa[m, b] * sb[g, n / 128, b] * (a[m, b] . b[g, n, b])
 //
-// Bounds.  Few rows: the weights' bytes (HBM; 512 rows over 256 matrices of 4096 x 7168 786 us, 1.01 of
-// the measured copy rate), below some 50 MB of them the launch and the latency of one short wave of tiles (one
-// row by 4096 x 7168 7.9 us, 4.3 of them the bytes).  Many rows: the promotion, and close behind it the
-// operands' way into the ring (32768 x 4096 x 7168 692 us, 2.8 PFLOP/s; the products alone 424 us, with
+// Bounds.  Few rows: the weights' bytes (HBM; 512 rows over 256 matrices of 4096 x 7168, 206 of them
+// with a row, 786 us, 7.7 TB/s), below some 50 MB of them the launch and the latency of one short wave of tiles
+// (one row by 4096 x 7168 7.9 us, 4.3 of them the bytes).  Many rows: the promotion, and close behind it the
+// operands' way into the ring (32768 x 4096 x 7168 689 us, 2.8 PFLOP/s; the products alone 424 us, with
 // their operands 592, with the promotion and no operands 640; the tensor cores are busy in half of the
 // cycles).
 //
@@ -669,7 +669,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 #pragma unroll
             for (int c = 0; c < 64; ++c) acc[c] = make_float2(0.f, 0.f);
             float s[4];
-#pragma unroll 8
+#pragma unroll 2
             for (int k = 0; k < a.kb; ++k) {
                 const uint32_t buf = it & 1, from = tmem_base + buf * kWideN + lanes;
                 if (!mbar_wait(pfull0 + 8 * buf, (it >> 1) & 1, abort_flag, status)) { ok = false; break; }
@@ -715,8 +715,14 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             const int m = done.m0 + quad * 32;                 // the warp's first row
             const int valid = min(32, done.rows - quad * 32);  // and how many count
             // (16-byte part c of a box's row r lies at place c ^ (r & 7), the swizzle of the tensor map)
+            uint32_t mine = smem_u32(way_out) + lane * 128, swizzle = (lane & 7) << 4;
+            // (made here: the compiler would keep all sixteen addresses through the k-steps, which have no
+            // register to spare)
+            asm volatile("" : "+r"(mine), "+r"(swizzle));
             auto put = [&](int c, uint4 v) {
-                *reinterpret_cast<uint4 *>(way_out + (c >> 3) * 4096 + lane * 128 + (((c ^ lane) & 7) << 4)) = v;
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(mine + (c >> 3) * 4096 + (((c & 7) << 4) ^ swizzle)),
+                             "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                             : "memory");
             };
             auto room = [&] {
                 if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
