@@ -749,20 +749,21 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 if (a.out_map && n * size % 16 == 0) {         // two rows at a time, 16 bytes to a lane
                     const int at = (lane & 15) * 16;
                     if (at < n * size)
-#pragma unroll 8
+#pragma unroll 4
                         for (int r = lane >> 4; r < valid; r += 2)
                             *reinterpret_cast<uint4 *>(to + r * a.out_stride * size + at) = *reinterpret_cast<const uint4 *>(
                                 way_out + (at >> 7) * 4096 + r * 128 + ((at & 127) ^ ((r & 7) << 4)));
                     __syncwarp();
                     return;
                 }
+                const bool word = !(((uint32_t)reinterpret_cast<uintptr_t>(a.out) | (uint32_t)(a.out_stride * size) |
+                                     (uint32_t)(n * size)) & 3);   // four bytes to a lane
                 for (int r = 0; r < valid; ++r)
-                    for (int c = lane; c < n; c += 32) {
-                        const int at = c * size;
+                    for (int at = lane * (word ? 4 : size); at < n * size; at += word ? 128 : 32 * size) {
                         const uint8_t *from = way_out + (at >> 7) * 4096 + r * 128 + ((at & 127) ^ ((r & 7) << 4));
-                        uint8_t *there = to + (r * a.out_stride + c) * size;
-                        if (size == 2) *reinterpret_cast<uint16_t *>(there) = *reinterpret_cast<const uint16_t *>(from);
-                        else *reinterpret_cast<uint32_t *>(there) = *reinterpret_cast<const uint32_t *>(from);
+                        uint8_t *there = to + r * a.out_stride * size + at;
+                        if (word) *reinterpret_cast<uint32_t *>(there) = *reinterpret_cast<const uint32_t *>(from);
+                        else *reinterpret_cast<uint16_t *>(there) = *reinterpret_cast<const uint16_t *>(from);
                     }
                 __syncwarp();
             };

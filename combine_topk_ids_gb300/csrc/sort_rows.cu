@@ -24,6 +24,7 @@ struct SortArgs {
     int32_t *hist;            // [nb][E] picks of each block and expert, then [nb] bad ids
 };
 
+constexpr int kHeld = 4;                    // picks of a lane that stay in registers
 constexpr int kMaxSortBlocks = 152;
 constexpr int kMaxSortCounts = 152 * 256;   // nb * E: every block reads all of them
 
@@ -43,6 +44,7 @@ __global__ void __launch_bounds__(512) sort_count_kernel(SortArgs a) {
     __syncthreads();
     const int64_t p0 = a.chunk * blockIdx.x, p1 = min(p0 + a.chunk, a.P);
     bool bad = false;
+#pragma unroll 4
     for (int64_t i = p0 + threadIdx.x; i < p1; i += blockDim.x) {
         const int e = expert_of(a, i, bad);
         if (e >= 0) atomicAdd(&hist[e], 1);
@@ -70,12 +72,28 @@ __global__ void __launch_bounds__(1024) sort_assign_kernel(SortArgs a) {
     pdl_wait();   // (for the counts, and for the ids)
     __syncthreads();
     bool bad = false;
-    for (int64_t i0 = w0; i0 < w1; i0 += 32) {
-        const int e = i0 + lane < w1 ? expert_of(a, i0 + lane, bad) : -1;
+    // the experts of a run of up to 128 picks stay in registers
+    const bool held = run <= 32 * kHeld;
+    int mine[kHeld];
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h) {
+        const int64_t i = w0 + 32 * h + lane;
+        mine[h] = held && i < w1 ? expert_of(a, i, bad) : -1;
+    }
+    auto each = [&](auto &&f) {   // f(pick, its expert or -1), 32 at a time
+        if (held) {
+#pragma unroll
+            for (int h = 0; h < kHeld; ++h)
+                if (w0 + 32 * h < w1) f(w0 + 32 * h + lane, mine[h]);
+        } else
+            for (int64_t i0 = w0; i0 < w1; i0 += 32)
+                f(i0 + lane, i0 + lane < w1 ? expert_of(a, i0 + lane, bad) : -1);
+    };
+    each([&](int64_t, int e) {
         const unsigned peers = __match_any_sync(kAllLanes, e);
         if (e >= 0 && lane == __ffs(peers) - 1) cur[warp * E + e] += __popc(peers);
         __syncwarp();
-    }
+    });
     if (a.nb > 1) {   // counts of all blocks, and of those before this one
         const int wide = (E + 31) / 32 * 32, slices = max(1, (int)blockDim.x / wide);
         for (int i = threadIdx.x; i < slices * wide; i += blockDim.x) {
@@ -134,9 +152,7 @@ __global__ void __launch_bounds__(1024) sort_assign_kernel(SortArgs a) {
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) a.offsets[E] = carry;
     const unsigned below = (1u << lane) - 1u;
-    for (int64_t i0 = w0; i0 < w1; i0 += 32) {
-        const int64_t i = i0 + lane;
-        const int e = i < w1 ? expert_of(a, i, bad) : -1;
+    each([&](int64_t i, int e) {
         const unsigned peers = __match_any_sync(kAllLanes, e);
         const int at = e >= 0 ? cur[warp * E + e] + __popc(peers & below) : -1;
         __syncwarp();
@@ -149,7 +165,7 @@ __global__ void __launch_bounds__(1024) sort_assign_kernel(SortArgs a) {
                 if (i >= carry) a.source[i] = -1;   // behind the last row
             }
         }
-    }
+    });
 }
 
 int sort_blocks(const moe_sort &g) {
@@ -263,6 +279,29 @@ __global__ void __launch_bounds__(kRowThreads) sort_rows_kernel(CopyArgs a) {
     else
         copy_piece(a, a.xs + t * a.scales, reinterpret_cast<char *>(a.rs), (int64_t)a.scales * 4, a.scales,
                    piece - a.nchunk, t);
+}
+
+// Rows of up to 16 words: LANES lanes to a token (and its scales, at most as many).  A warp to a piece
+// would leave most lanes without work, and its picks' stores would follow one another.
+template <typename W, int LANES>
+__global__ void __launch_bounds__(kRowThreads) sort_short_rows_kernel(CopyArgs a) {
+    pdl_wait();
+    const int64_t t = ((int64_t)blockIdx.x * kRowThreads + threadIdx.x) / LANES;
+    const int lane = threadIdx.x % LANES;
+    if (t >= a.T) return;
+    const bool word = lane < a.words, scale = lane < a.scales;
+    W v;
+    float s;
+    if (word) v = reinterpret_cast<const W *>(a.x + t * a.xstride)[lane];
+    if (scale) s = a.xs[t * a.scales + lane];
+    const int32_t *pos = a.position + t * a.k;
+#pragma unroll 4
+    for (int j = 0; j < a.k; ++j) {
+        const int p = pos[j];
+        if (p < 0 || p >= a.num_rows) continue;
+        if (word) reinterpret_cast<W *>(a.rows + p * a.rstride)[lane] = v;
+        if (scale) a.rs[(int64_t)p * a.scales + lane] = s;
+    }
 }
 
 struct SumArgs {
@@ -575,9 +614,19 @@ extern "C" int moe_sort_rows(const moe_rows *g, const void *x_dev, const float *
     const int piece = 32 * (word == 16 ? kCopyWords<uint4> : kCopyWords<uint32_t>);
     a.nchunk = (a.words + piece - 1) / piece;
     a.nchunk_all = a.nchunk + (a.scales + 32 * kCopyWords<float> - 1) / (32 * kCopyWords<float>);
-    const int64_t blocks = blocks_of((int64_t)a.T * a.nchunk_all);
+    const bool brief = a.words <= 16;
+    const int lanes = a.words <= 4 ? 4 : a.words <= 8 ? 8 : 16;
+    const int64_t blocks = brief ? ((int64_t)a.T * lanes + kRowThreads - 1) / kRowThreads
+                                 : blocks_of((int64_t)a.T * a.nchunk_all);
     if (blocks >= ((int64_t)1 << 31)) return MOE_ERR_LIMIT;
     auto launch = [&](auto w) {
+        using W = decltype(w);
+        if (brief) {
+            auto *kernel = lanes == 4 ? sort_short_rows_kernel<W, 4> : lanes == 8 ? sort_short_rows_kernel<W, 8>
+                                                                                 : sort_short_rows_kernel<W, 16>;
+            return status_of(launch_pdl(kernel, dim3((unsigned)blocks), dim3(kRowThreads), 0,
+                                        static_cast<cudaStream_t>(stream), a));
+        }
         return status_of(launch_pdl(sort_rows_kernel<decltype(w)>, dim3((unsigned)blocks), dim3(kRowThreads), 0,
                                     static_cast<cudaStream_t>(stream), a));
     };
