@@ -25,6 +25,7 @@ struct SortArgs {
 };
 
 constexpr int kHeld = 4;                    // picks of a lane that stay in registers
+constexpr int kLeastRun = 64;              // picks of a warp, before there is another warp's counts to add
 constexpr int kMaxSortBlocks = 152;
 constexpr int kMaxSortCounts = 152 * 256;   // nb * E: every block reads all of them
 
@@ -54,8 +55,9 @@ __global__ void __launch_bounds__(512) sort_count_kernel(SortArgs a) {
     if (threadIdx.x == 0) a.hist[(int64_t)a.nb * a.E + blockIdx.x] = bad;
 }
 
-// Up to 4096 picks one block does it all (512 picks over 256 experts: 4 us of latency); above, every
-// block counts its picks first, and then reads the counts of all (262144 picks: 15 us in both kernels).
+// Up to 1024 picks one block does it all; above, every block of 512 or more picks counts them first, and
+// then reads the counts of all.  Measured with 256 experts, us: 512 picks 3.7, 1024 6.2 (in two kernels
+// 6.6), 2048 6.5 (one block 8.6), 4096 7.0 (13), 32768 7.7, 262144 13.6.
 //
 // Each warp owns a contiguous run of the block's picks: it counts the run by expert, the counts
 // become the first position of its run in each expert, and then it ranks the run 32 at a time.
@@ -64,7 +66,8 @@ __global__ void __launch_bounds__(1024) sort_assign_kernel(SortArgs a) {
     __shared__ int wsum[32];
     const int E = a.E, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int64_t p0 = min(a.chunk * blockIdx.x, a.P), p1 = min(p0 + a.chunk, a.P);
-    const int64_t run = ((p1 - p0 + warps - 1) / warps + 31) / 32 * 32;
+    int64_t run = ((p1 - p0 + warps - 1) / warps + 31) / 32 * 32;
+    if (run < kLeastRun) run = kLeastRun;
     const int used = run ? (int)((p1 - p0 + run - 1) / run) : 0;   // warps with a run
     const int64_t w0 = min(p0 + warp * run, p1), w1 = min(w0 + run, p1);
     int *total = sm, *before = sm + E, *cur = sm + 2 * E;          // cur [used][E]
@@ -122,6 +125,7 @@ __global__ void __launch_bounds__(1024) sort_assign_kernel(SortArgs a) {
         if (e < E) {
             if (a.nb > 1) n = total[e];
             else
+#pragma unroll 8
                 for (int w = 0; w < used; ++w) n += cur[w * E + e];
         }
         int incl = n;
@@ -141,10 +145,15 @@ __global__ void __launch_bounds__(1024) sort_assign_kernel(SortArgs a) {
             const int first = ahead + incl - n;
             if (blockIdx.x == 0) a.offsets[e] = first;
             int at = first + before[e];
-            for (int w = 0; w < used; ++w) {
-                const int c = cur[w * E + e];
-                cur[w * E + e] = at;
-                at += c;
+            for (int w = 0; w < used; w += 8) {   // (eight at a time: their loads do not wait for the stores)
+                int c[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) c[i] = w + i < used ? cur[(w + i) * E + e] : 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if (w + i < used) cur[(w + i) * E + e] = at;
+                    at += c[i];
+                }
             }
         }
         carry += block_sum;
@@ -170,8 +179,8 @@ __global__ void __launch_bounds__(1024) sort_assign_kernel(SortArgs a) {
 
 int sort_blocks(const moe_sort &g) {
     const int64_t P = (int64_t)g.num_tokens * g.top_k;
-    if (P <= 4096) return 1;
-    int64_t nb = (P + 2047) / 2048;
+    if (P <= 1024) return 1;
+    int64_t nb = (P + 511) / 512;
     if (nb > kMaxSortBlocks) nb = kMaxSortBlocks;
     if (nb * g.num_experts > kMaxSortCounts) nb = kMaxSortCounts / g.num_experts;
     return (int)nb;
@@ -569,15 +578,15 @@ extern "C" int moe_sort_picks(const moe_sort *g, const void *topk_ids_dev, int i
     if (a.nb > 1 &&
         (e = launch_pdl(sort_count_kernel, dim3(a.nb), dim3(512), (size_t)a.E * 4, s, a)) != cudaSuccess)
         return status_of(e);
-    // one table row for each warp with picks: 128 KB at most
-    int warps = a.E <= 1024 ? 32 : 16;
-    const int64_t need = (a.chunk + 31) / 32;
-    if (need < warps) warps = need < 8 ? 8 : (int)need;
-    const size_t smem = (size_t)(2 + warps) * a.E * 4;
+    // one table row for each warp with picks: 128 KB at most.  All warps read the blocks' counts.
+    const int warps = a.E <= 1024 ? 32 : 16;
+    const int64_t need = (a.chunk + kLeastRun - 1) / kLeastRun;
+    const int rows = need < warps ? (int)need : warps, threads = a.nb > 1 || rows > 8 ? 32 * warps : 256;
+    const size_t smem = (size_t)(2 + rows) * a.E * 4;
     if (smem > 48 * 1024 && (e = cudaFuncSetAttribute(sort_assign_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                       (int)smem)) != cudaSuccess)
         return status_of(e);
-    return status_of(launch_pdl(sort_assign_kernel, dim3(a.nb), dim3(32 * warps), smem, s, a));
+    return status_of(launch_pdl(sort_assign_kernel, dim3(a.nb), dim3(threads), smem, s, a));
 }
 
 extern "C" int moe_sort_rows(const moe_rows *g, const void *x_dev, const float *x_scales_dev,
