@@ -16,9 +16,11 @@
 //
 // product_fp8_kernel computes tiles of 128 output columns and NT rows.  The weights are the M side of
 // the products and the rows the N side, so that few rows cost few columns of tensor memory: a lane
-// has one output column, a register one row.  192 threads:
+// has one output column, a register one row.  256 threads:
 //   warp 0      fills a ring of stages (128 x 128 weights, NT x 128 rows) with TMA
-//   warp 1      issues the products, each k-step into the next of several buffers in tensor memory
+//   warps 1, 6  issue the products, one the even k-steps and one the odd ones, each k-step into the next
+//               of several buffers in tensor memory.  (One thread's waits and issues for all of them take
+//               longer than the products.)
 //   warps 2-5   promotion
 //   warp 7      puts the scales' products of the next eight k-steps into shared memory: a promoting warp
 //               that had loads of its own under way would wait for them with its tensor-memory loads
@@ -37,7 +39,7 @@ constexpr int kBK = 128;            // inner columns (bytes) of a k-step
 constexpr int kTileN = 128;         // output columns of a tile: one block of the weights' scales
 constexpr int kThreads = 256;
 constexpr int kScaleSteps = 8;      // k-steps of one table of scales
-constexpr int kMaxSplit = 8;        // blocks that share a tile (what any GPU's clusters hold)
+constexpr int kMaxSplit = 8;        // blocks that share a tile (the portable size of a cluster)
 
 struct ProductArgs {
     const float *sa, *sb;
