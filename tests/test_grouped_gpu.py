@@ -1,6 +1,8 @@
 """The operators on expert-grouped rows on the GPU, through the public entry points, against the
 float64 oracle, at the sizes, strides and masks where they can go wrong."""
 import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -11,6 +13,7 @@ from oracle import fp8 as ofp8
 from oracle import grouped as og
 from oracle.block import BF16, E4M3, EPS32
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 pytestmark = pytest.mark.gpu
 BF, F32, I32, F8 = torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn
 HALF = {BF: BF16, F32: EPS32}
@@ -402,6 +405,20 @@ def test_grouped_product(T, k, E, N, K, drop, skew):
     assert (out[off[-1]:] == 7).all()
 
 
+@pytest.mark.parametrize("M,N,K", [(5, 384, 256), (200, 256, 640)])
+def test_product_gradient_of_the_rows(M, N, K):
+    """d(a) of out = a b^T is the product of out's gradient and the transposed codes and scales."""
+    dy, sy = codes_of(M, N, block=1, seed=1)
+    b, sb = codes_of(N, K, block=128, seed=2)
+    da = torch.empty((M, K), device="cuda")
+    moe.moe_product_fp8(dy, sy, b.view(torch.uint8).t().contiguous(), sb.t().contiguous(), da)
+    w = ofp8.decode_e4m3(b.view(torch.uint8).cpu().numpy()) * np.repeat(np.repeat(f64(sb), 128, 0), 128, 1)
+    g = ofp8.decode_e4m3(dy.view(torch.uint8).cpu().numpy()) * np.repeat(f64(sy), 128, 1)
+    size = np.abs(g) @ np.abs(w)
+    bound = (128 * 2.0 ** -23 + (N // 128 + 5) * EPS32) * size
+    within(f64(da), g @ w, bound + EPS32 * size, "da")
+
+
 def test_product_offsets_of_all_kinds():
     """Rows in front of the first group, empty groups, offsets beyond the rows: as if clamped."""
     M, N, K = 70, 130, 256
@@ -556,6 +573,36 @@ def test_streams_and_graphs():
         torch.cuda.synchronize()
         for i in range(2):
             assert torch.equal(chains[i].out, want[turn + i])
+
+
+def test_first_calls_inside_a_capture():
+    """A process whose first calls are captured: what is set up once is set up there too."""
+    code = """
+import sys, torch
+sys.path.insert(0, %r)
+import combine_topk_ids_gb300 as moe
+z = lambda *s, dtype=torch.float32: torch.zeros(s, dtype=dtype, device="cuda")
+F8, I32 = torch.float8_e4m3fn, torch.int32
+ids, off, pos = torch.randint(0, 1000, (600, 4), device="cuda"), z(1001, dtype=I32), z(600, 4, dtype=I32)
+work = z(moe.moe_sort_picks_workspace_size(600, 4, 1000), dtype=torch.uint8)
+x, codes, scales = torch.randn(2600, 256, device="cuda"), z(2600, 256, dtype=F8), z(2600, 2)
+b, bs, wide, few = torch.ones(2304, 256, device="cuda").to(F8), z(18, 2) + 1, z(2600, 2304), z(3, 2304)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    moe.moe_sort_picks(ids, 1000, off, pos, work)
+    moe.moe_quantize_fp8(x, codes, scales)
+    moe.moe_product_fp8(codes, scales, b, bs, wide)
+    moe.moe_product_fp8(codes[:3], scales[:3], b, bs, few)
+for _ in range(2):
+    g.replay()
+torch.cuda.synchronize()
+v = (codes.float() * scales.repeat_interleave(128, 1)).double().sum(1)
+assert off[-1] == 2400 and ((wide.double() - v[:, None]).abs() < 1e-3).all() and torch.equal(few, wide[:3])
+print("captured")
+""" % ROOT
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=200)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
 
 
 def test_gradient_reaches_the_router():
