@@ -392,14 +392,15 @@ struct BackArgs {
     int T, k, H, num_rows;
 };
 
-template <int N> constexpr int kBackUnits = N == 1 ? 4 : 1;   // accesses of a thread and row under way
+template <int N> constexpr int kBackUnits = N == 1 ? 8 : 1;   // accesses of a thread and row under way
 
 // blockDim.x threads to a token, blockDim.y tokens to a block; P picks share a reading of dout.  A warp to
 // a token where there are tokens enough: 16381 x 2048 bf16, top-4, 86 us (0.95 of the copy rate; a block to
-// a token 168).  Rows off 16-byte boundaries column by column, four of a lane under way for each pick
-// (x 2047 160 us, 0.5: the schedulers issue in 67% of the cycles; one column 186, eight 203).
+// a token 168).  Rows off 16-byte boundaries column by column, eight of a lane under way for each pick, at
+// fixed distances from one address (x 2047 118 us, 0.69: latency, with the schedulers issuing in 42% of
+// the cycles and DRAM at 57%; at distances that hang on the block's size 160, one column 186).
 template <typename R, typename O, int N, int P>
-__global__ void __launch_bounds__(256) unsort_rows_backward_kernel(BackArgs a) {
+__global__ void __launch_bounds__(256, N == 1 ? 3 : 0) unsort_rows_backward_kernel(BackArgs a) {
     constexpr int U = kBackUnits<N>;
     __shared__ float red[8][P];
     pdl_wait();
@@ -420,12 +421,12 @@ __global__ void __launch_bounds__(256) unsort_rows_backward_kernel(BackArgs a) {
             w[q] = p[q] >= 0 && a.w ? a.w[t * a.k + j0 + q] : 1.f;
             dot[q] = 0.f;
         }
-        for (int c0 = threadIdx.x * N; live && c0 < a.H; c0 += blockDim.x * N * U) {
+        for (int c0 = ((threadIdx.x >> 5) * 32 * U + lane) * N; live && c0 < a.H; c0 += blockDim.x * N * U) {
             Pack<O, N> d[U];
             Pack<R, N> v[P][U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int c = c0 + u * blockDim.x * N;
+                const int c = c0 + 32 * N * u;
                 if (c < a.H) d[u].load(dout + c);
             }
             if (a.dw) {
@@ -434,7 +435,7 @@ __global__ void __launch_bounds__(256) unsort_rows_backward_kernel(BackArgs a) {
                     if (p[q] >= 0)
 #pragma unroll
                         for (int u = 0; u < U; ++u) {
-                            const int c = c0 + u * blockDim.x * N;
+                            const int c = c0 + 32 * N * u;
                             if (c < a.H) v[q][u].load(rows + p[q] * a.rstride + c);
                         }
             }
@@ -444,7 +445,7 @@ __global__ void __launch_bounds__(256) unsort_rows_backward_kernel(BackArgs a) {
                     if (p[q] >= 0)
 #pragma unroll
                         for (int u = 0; u < U; ++u) {
-                            const int c = c0 + u * blockDim.x * N;
+                            const int c = c0 + 32 * N * u;
                             float g[N];
 #pragma unroll
                             for (int n = 0; n < N; ++n) g[n] = w[q] * d[u].at(n);
@@ -457,7 +458,7 @@ __global__ void __launch_bounds__(256) unsort_rows_backward_kernel(BackArgs a) {
                     if (p[q] >= 0)
 #pragma unroll
                         for (int u = 0; u < U; ++u)
-                            if (c0 + u * blockDim.x * N < a.H)
+                            if (c0 + 32 * N * u < a.H)
 #pragma unroll
                                 for (int n = 0; n < N; ++n) dot[q] = fmaf(d[u].at(n), v[q][u].at(n), dot[q]);
             }
@@ -704,6 +705,9 @@ extern "C" int moe_unsort_rows_backward(const moe_rows *g, const void *dout_dev,
         };
         using R = decltype(r);
         using O = decltype(o);
-        return a.k <= 4 ? launch(unsort_rows_backward_kernel<R, O, N, 4>) : launch(unsort_rows_backward_kernel<R, O, N, 8>);
+        // single columns four picks at a time for any k: eight picks leave registers for four columns only
+        // (8192 x 2047, top-8, 165 us; as here 132)
+        if constexpr (N == 1) return launch(unsort_rows_backward_kernel<R, O, N, 4>);
+        else return a.k <= 4 ? launch(unsort_rows_backward_kernel<R, O, N, 4>) : launch(unsort_rows_backward_kernel<R, O, N, 8>);
     });
 }
