@@ -107,7 +107,9 @@ typedef struct {
  *   ceil(num_rows / block_rows), cols / 128].  A value that is not a number gets the code of NaN and does not touch
  *   its block's scale; an infinity makes its whole block NaN.
  * moe_swiglu_fp8 - v = silu(gate) * up of gate_up [matrices, num_rows, 2 * cols] (the gate in the first half
- *   of the columns) in float32, quantised the same way (block_rows 1).  silu(g) = g / (1 + exp(-g)).
+ *   of the columns) in float32, quantised the same way (block_rows 1).  silu(g) = g / (1 + exp(-g)); where
+ *   1 / (1 + exp(-g)) is below 2^-126, the smallest normal float32 (finite g below -87.3), silu is 0.  At
+ *   g = -infinity the formula is not a number, which marks that column's code alone.
  * live_rows_dev: one int32 in device memory, or NULL: only the first that many rows are taken,
  *   the outputs of those behind are left as they were (with moe_sort_picks: &offsets[num_experts]).
  *   It has to be NULL with block_rows 128 or several matrices.
