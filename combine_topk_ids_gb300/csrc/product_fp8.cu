@@ -825,21 +825,6 @@ bool make_codes_map(CUtensorMap *m, const void *base, int64_t rows, int64_t cols
     return make_rows_map(m, base, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, rows, cols, stride, box_rows);
 }
 
-// A kernel's shared memory, allowed once on each device (with that device current).
-struct PerDevice {
-    std::once_flag once[64];
-    cudaError_t error[64];
-    template <typename K, typename F> cudaError_t set(K kernel, int smem, F &&more) {
-        const int d = device_ordinal();
-        if (d < 0) return cudaErrorInvalidDevice;
-        std::call_once(once[d], [&] {
-            error[d] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-            if (error[d] == cudaSuccess) error[d] = more(d);
-        });
-        return error[d];
-    }
-};
-
 // Clusters of `cluster` blocks (1: none), after the kernel before it in the stream.
 template <typename K, typename... Args>
 int launch_clusters(K kernel, int64_t grid, int cluster, int threads, int smem, cudaStream_t s, const Args &...args) {

@@ -29,6 +29,11 @@ constexpr int kLeastRun = 64;              // picks of a warp, before there is a
 constexpr int kMaxSortBlocks = 152;
 constexpr int kMaxSortCounts = 152 * 256;   // nb * E: every block reads all of them
 
+// Most warps of a block of sort_assign_kernel, and the most that its table of a row for each (and two more) takes.
+constexpr int sort_warps(int E) { return E <= 1024 ? 32 : 16; }
+constexpr int kMostTable = (2 + sort_warps(MOE_MAX_EXPERTS)) * MOE_MAX_EXPERTS * 4;
+static_assert(kMostTable >= (2 + sort_warps(1024)) * 1024 * 4, "the most experts take the largest table");
+
 // Expert of pick i, -1 where it is masked or dropped.
 __device__ __forceinline__ int expert_of(const SortArgs &a, int64_t i, bool &bad) {
     const long long v = a.ids64 ? static_cast<const long long *>(a.ids)[i] : static_cast<const int *>(a.ids)[i];
@@ -55,9 +60,10 @@ __global__ void __launch_bounds__(512) sort_count_kernel(SortArgs a) {
     if (threadIdx.x == 0) a.hist[(int64_t)a.nb * a.E + blockIdx.x] = bad;
 }
 
-// Up to 1024 picks one block does it all; above, every block of 512 or more picks counts them first, and
-// then reads the counts of all.  Measured with 256 experts, us: 512 picks 3.7, 1024 6.2 (in two kernels
-// 6.6), 2048 6.5 (one block 8.6), 4096 7.0 (13), 32768 7.7, 262144 13.6.
+// Up to 1024 picks one block does it all.  Above, blocks of up to 512 picks (more where that would take over
+// 152 blocks, or counts over kMaxSortCounts) count theirs first, and then each reads the counts of all.
+// Measured with 256 experts, us: 512 picks 3.7, 1024 6.2 (in two kernels 6.6), 2048 6.5 (one block 8.6),
+// 4096 7.0 (13), 32768 7.7, 262144 13.6.
 //
 // Each warp owns a contiguous run of the block's picks: it counts the run by expert, the counts
 // become the first position of its run in each expert, and then it ranks the run 32 at a time.
@@ -575,18 +581,17 @@ extern "C" int moe_sort_picks(const moe_sort *g, const void *topk_ids_dev, int i
     a.offsets = offsets_dev; a.position = position_dev; a.source = source_dev; a.status = status_dev;
     a.hist = static_cast<int32_t *>(workspace_dev);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e;
+    static PerDevice devices;
+    cudaError_t e = devices.set(sort_assign_kernel, kMostTable, [](int) { return cudaSuccess; });
+    if (e != cudaSuccess) return status_of(e);
     if (a.nb > 1 &&
         (e = launch_pdl(sort_count_kernel, dim3(a.nb), dim3(512), (size_t)a.E * 4, s, a)) != cudaSuccess)
         return status_of(e);
-    // one table row for each warp with picks: 128 KB at most.  All warps read the blocks' counts.
-    const int warps = a.E <= 1024 ? 32 : 16;
+    // one table row for each warp with picks.  All warps read the blocks' counts.
+    const int warps = sort_warps(a.E);
     const int64_t need = (a.chunk + kLeastRun - 1) / kLeastRun;
     const int rows = need < warps ? (int)need : warps, threads = a.nb > 1 || rows > 8 ? 32 * warps : 256;
     const size_t smem = (size_t)(2 + rows) * a.E * 4;
-    if (smem > 48 * 1024 && (e = cudaFuncSetAttribute(sort_assign_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                      (int)smem)) != cudaSuccess)
-        return status_of(e);
     return status_of(launch_pdl(sort_assign_kernel, dim3(a.nb), dim3(threads), smem, s, a));
 }
 
