@@ -6,7 +6,6 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
-#include <mutex>
 
 #include "../../include/moe_block.h"
 #include "moe_internal.cuh"
@@ -39,23 +38,6 @@ __device__ __forceinline__ float warp_sum(float v) {
     for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(kAllLanes, v, o);
     return v;
 }
-
-// A kernel's shared memory, allowed once on each device (with that device current): the most that any call
-// takes, since the amount belongs to the kernel on the device and not to the call.  A call that set its own would
-// take it from another host thread's between that one's setting and its launch.
-struct PerDevice {
-    std::once_flag once[64];
-    cudaError_t error[64];
-    template <typename K, typename F> cudaError_t set(K kernel, int smem, F &&more) {
-        const int d = device_ordinal();
-        if (d < 0) return cudaErrorInvalidDevice;
-        std::call_once(once[d], [&] {
-            error[d] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-            if (error[d] == cudaSuccess) error[d] = more(d);
-        });
-        return error[d];
-    }
-};
 
 }  // namespace
 }  // namespace moe

@@ -4,6 +4,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <mutex>
 #include <cuda_runtime.h>
 
 #include "../../include/moe.h"
@@ -99,6 +100,23 @@ int launch_gemm2_fp8(const Routing &r, const uint8_t *w2q, const float *w2s, voi
 int num_sms();   // SM count of the current device (cached per device)
 int check_device();   // MOE_OK on a compute capability 10.3 device, else a moe_error
 int device_ordinal();   // the current device, or -1 (only ordinals below 64 are served)
+
+// A kernel's shared memory, allowed once on each device (with that device current): the most that any call
+// takes, since the amount belongs to the kernel on the device and not to the call.  A call that set its own would
+// take it from another host thread's between that one's setting and its launch.
+struct PerDevice {
+    std::once_flag once[64];
+    cudaError_t error[64];
+    template <typename K, typename F> cudaError_t set(K kernel, int smem, F &&more) {
+        const int d = device_ordinal();
+        if (d < 0) return cudaErrorInvalidDevice;
+        std::call_once(once[d], [&] {
+            error[d] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (error[d] == cudaSuccess) error[d] = more(d);
+        });
+        return error[d];
+    }
+};
 
 // ---- programmatic dependent launch -----------------------------------------------------
 // The layer's kernels are launched with programmatic stream serialization, so the launch of

@@ -613,12 +613,15 @@ __global__ void __launch_bounds__(kFusedThreads) route_fused_kernel(RouteArgs a)
 #ifndef MOE_FUSED_ROUTING_MAX_PICKS
 #define MOE_FUSED_ROUTING_MAX_PICKS 3072
 #endif
+constexpr int kFusedExperts = 64;   // most experts of the single-CTA path
+// Its shared memory in ints.
+constexpr size_t fused_ints(int E, int W) { return (size_t)kFusedWarps * (E + W) + E * W + W * W + 2 * E; }
 // The single-CTA path wins for small batches over few experts (one launch instead of
 // three: 9-12 vs 14-15 us for 128-2048 picks) and loses for larger ones (44.6 vs 15.9 us
 // on 16384 picks over 16 experts; 82 vs 36 us with 256 experts, where its per-expert work
 // runs on one SM), so it is kept for at most 3072 picks and E <= 64.
 int routing_launches(const Plan &p) {
-    return (p.P <= MOE_FUSED_ROUTING_MAX_PICKS && p.E <= 64 && p.E * p.W <= 4096) ? 1 : 3;
+    return (p.P <= MOE_FUSED_ROUTING_MAX_PICKS && p.E <= kFusedExperts && p.E * p.W <= 4096) ? 1 : 3;
 }
 
 cudaError_t launch_routing(const Routing &r, const void *ids, int ids64, const float *topk_w,
@@ -648,31 +651,28 @@ cudaError_t launch_routing(const Routing &r, const void *ids, int ids64, const f
     // the status word itself (one launch less in a latency-bound step)
     if (routing_launches(p) == 1) {
         a.zero_status = 1;
-        const size_t smf = (size_t)(kFusedWarps * (a.E + a.W) + a.E * a.W + a.W * a.W + 2 * a.E) *
-                           sizeof(int);
-        if (smf > 48 * 1024) {
-            cudaError_t e = cudaFuncSetAttribute(route_fused_kernel,
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smf);
-            if (e != cudaSuccess) return e;
-        }
+        const size_t smf = fused_ints(a.E, a.W) * sizeof(int);
+        static PerDevice devices;   // (for the most experts and ranks that go this way)
+        const cudaError_t e = devices.set(route_fused_kernel, (int)(fused_ints(kFusedExperts, MOE_MAX_WORLD) * sizeof(int)),
+                                          [](int) { return cudaSuccess; });
+        if (e != cudaSuccess) return e;
         return launch_pdl(route_fused_kernel, dim3(1), dim3(kFusedThreads), smf, s, a);
     }
 
+    static PerDevice devices;
+    cudaError_t e = devices.set(route_assign_kernel, (int)(kRouteWarps * (MOE_MAX_EXPERTS + MOE_MAX_WORLD) * sizeof(int)),
+                                [](int) { return cudaSuccess; });
+    if (e != cudaSuccess) return e;
     // several blocks may raise status bits: clear the word before the first of them runs
     // (the GEMMs' tile counters follow the status word when there is a workspace)
     if (cudaMemsetAsync(a.status, 0, (r.sched ? 5 : 1) * sizeof(int32_t), s) != cudaSuccess)
         return cudaGetLastError();
     size_t sm1 = (size_t)(a.E + a.W) * sizeof(int);
-    cudaError_t e = launch_pdl(route_count_kernel, dim3(a.nb), dim3(kRouteThreads), sm1, s, a);
+    e = launch_pdl(route_count_kernel, dim3(a.nb), dim3(kRouteThreads), sm1, s, a);
     if (e != cudaSuccess) return e;
     e = launch_pdl(route_scan_kernel, dim3(1), dim3(1024), 0, s, a);
     if (e != cudaSuccess) return e;
     size_t sm3 = (size_t)kRouteWarps * (a.E + a.W) * sizeof(int);
-    if (sm3 > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(route_assign_kernel,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm3);
-        if (e != cudaSuccess) return e;
-    }
     return launch_pdl(route_assign_kernel, dim3(a.nb), dim3(kRouteThreads), sm3, s, a);
 }
 
