@@ -89,6 +89,11 @@ def _refuse(t, name, dtypes, shape, dev, layout):
     raise ValueError("%s: strides %s; %s" % (name, t.stride(), layout))
 
 
+def _too_large(where):
+    """Raises for a size that the C structs' 32-bit fields do not hold: ctypes would cut it off without a word."""
+    _call(-13, where)   # MOE_ERR_LIMIT
+
+
 # Small calls take as long as their checks do on the host, so what is right is found out first.
 
 def _packed(t, name, dtypes, shape, dev):
@@ -148,6 +153,8 @@ def moe_add_rmsnorm(x, residual, weight, eps, sum_out=None, out=None, out_fp8=No
         raise ValueError("weight, and out or out_fp8 with scales, must be given")
     shape, dev = x.shape, x.get_device()
     T, H = shape
+    if (T | H) >> 31:
+        _too_large("moe_add_rmsnorm")
     px, xs = _rows(x, "x", _BF16, shape, dev)
     pr, rs = _rows(residual, "residual", _ROW, shape, dev)
     ps, ss = _rows(sum_out, "sum_out", _ROW if residual is None else (residual.dtype,), shape, dev)
@@ -164,6 +171,8 @@ def moe_add_rmsnorm(x, residual, weight, eps, sum_out=None, out=None, out_fp8=No
 def moe_add_rmsnorm_workspace_size(tokens, hidden):
     """Bytes of the workspace of moe_add_rmsnorm_backward."""
     size = ctypes.c_size_t()
+    if max(tokens, hidden) >> 31:
+        _too_large("moe_add_rmsnorm_workspace_size")
     _call(_lib().moe_add_rmsnorm_workspace_size(MoeNorm(tokens, hidden), ctypes.byref(size)),
           "moe_add_rmsnorm_workspace_size")
     return size.value
@@ -180,6 +189,8 @@ def moe_add_rmsnorm_backward(dout, h, weight, rstd, dx, dweight, workspace, dsum
     _typed(workspace, "workspace", _BYTE)
     shape, dev, same = dout.shape, dout.get_device(), (h.dtype,)
     T, H = shape
+    if (T | H) >> 31:
+        _too_large("moe_add_rmsnorm_backward")
     pg, gs = _rows(dout, "dout", _BF16, shape, dev)
     ph, hs = _rows(h, "h", same, shape, dev)
     ps, ss = _rows(dsum, "dsum", same, shape, dev)
@@ -209,6 +220,8 @@ def _route(r, logits):
     _typed(logits, "logits", _ROW)
     if logits.dim() != 2 or logits.shape[1] != r.num_experts:
         raise ValueError("logits: shape %s, expected [tokens, %d]" % (tuple(logits.shape), r.num_experts))
+    if logits.shape[0] >> 31:
+        _too_large("moe_route_topk")
     dev = logits.get_device()
     p, stride = _rows(logits, "logits", _ROW, logits.shape, dev)
     dtype = DTYPE[logits.dtype]

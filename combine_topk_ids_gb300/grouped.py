@@ -12,7 +12,8 @@ import ctypes
 
 import torch
 
-from .block import _BF16, _BYTE, _E4M3, _F32, _IDS, _P, _ROW, DTYPE, _call, _lib, _packed, _rows, _stream, _typed
+from .block import (_BYTE, _E4M3, _F32, _IDS, _P, _ROW, DTYPE, _call, _lib, _packed, _rows, _stream, _too_large,
+                    _typed)
 
 _I32 = (torch.int32,)
 _ROWS_CODES = _ROW + _E4M3
@@ -88,6 +89,8 @@ def _missing(names, *addresses):
 def moe_sort_picks_workspace_size(tokens, top_k, num_experts):
     """Bytes of the workspace of moe_sort_picks."""
     size = ctypes.c_size_t()
+    if max(tokens, top_k, num_experts) >> 31:
+        _too_large("moe_sort_picks_workspace_size")
     _call(_lib().moe_sort_picks_workspace_size(MoeSort(tokens, num_experts, top_k), ctypes.byref(size)),
           "moe_sort_picks_workspace_size")
     return size.value
@@ -100,6 +103,8 @@ def moe_sort_picks(topk_ids, num_experts, offsets, position, workspace, source=N
     int32 [1], MOE_STATUS_* bits (an id outside [-1, num_experts) is dropped).  workspace: uint8, of
     moe_sort_picks_workspace_size bytes."""
     (T, k), dev, pi = _packed_matrix(topk_ids, "topk_ids", _IDS)
+    if (T | k | num_experts) >> 31 > 0:
+        _too_large("moe_sort_picks")
     po = _packed(offsets, "offsets", _I32, (num_experts + 1,), dev)
     pp = _packed(position, "position", _I32, (T, k), dev)
     pw = None if workspace is None else _packed(workspace, "workspace", _BYTE, workspace.shape, dev)
@@ -120,6 +125,8 @@ def moe_sort_rows(x, position, rows, x_scales=None, rows_scales=None, stream=Non
     (T, H), dev, px, xs = _matrix(x, "x", _ROWS_CODES)
     (R, _), _, pr, rs = _matrix(rows, "rows", _ROWS_CODES)
     (t, k), _, pp = _packed_matrix(position, "position", _I32)
+    if (T | H | R | k) >> 31:
+        _too_large("moe_sort_rows")
     dtype, shape = _DTYPE[x.dtype], (R, H)
     if t != T or rows.shape != shape or rows.get_device() != dev or position.get_device() != dev or \
             _DTYPE[rows.dtype] != dtype:
@@ -143,6 +150,8 @@ def moe_sort_rows_backward(drows, position, dx, stream=None):
     """dx[t] = sum of drows[position[t, j]] over the token's picks (bf16 or float32 alike)."""
     (T, k), dev, pp = _packed_matrix(position, "position", _I32)
     (R, H), _, pr, rs = _matrix(drows, "drows", _ROW)
+    if (T | k | R | H) >> 31:
+        _too_large("moe_sort_rows_backward")
     if drows.get_device() != dev:
         _rows(drows, "drows", _ROW, drows.shape, dev)
     px, xs = _rows(dx, "dx", (drows.dtype,), (T, H), dev)
@@ -158,6 +167,8 @@ def moe_unsort_rows(rows, weights, position, out, stream=None):
     weights float32 [T, k], or None: all 1.  rows [R, H] and out [T, H] bf16 or float32 each."""
     (T, k), dev, pp = _packed_matrix(position, "position", _I32)
     (R, H), _, pr, rs = _matrix(rows, "rows", _ROW)
+    if (T | k | R | H) >> 31:
+        _too_large("moe_unsort_rows")
     if rows.get_device() != dev:
         _rows(rows, "rows", _ROW, rows.shape, dev)
     po, os = _rows(out, "out", _ROW, (T, H), dev)
@@ -182,6 +193,8 @@ def moe_unsort_rows_backward(dout, rows, weights, position, drows, dweights, str
     if drows is None and dweights is None:
         raise ValueError("drows or dweights must be given")
     R = _matrix(like, "drows" if rows is None else "rows", _ROW)[0][0]
+    if (T | k | R | H) >> 31:
+        _too_large("moe_unsort_rows_backward")
     pr, rs = _rows(rows, "rows", _ROW, (R, H), dev)
     pd, ds = _rows(drows, "drows", (like.dtype,), (R, H), dev)
     pw = _packed(weights, "weights", _F32, (T, k), dev)
@@ -206,6 +219,8 @@ def moe_quantize_fp8(x, codes, scales, block_rows=1, live_rows=None, stream=None
             raise ValueError("x: shape %s, expected rows" % (tuple(x.shape),))
         lead, (R, C), dev = x.shape[:-2], x.shape[-2:], x.get_device()
         px, xs, n = _packed(x, "x", _ROW, x.shape, dev), 0, lead.numel()
+    if (n | R | C) >> 31:
+        _too_large("moe_quantize_fp8")
     if block_rows not in (1, 128):
         raise ValueError("block_rows: %r, expected 1 or 128" % (block_rows,))
     pc = _packed(codes, "codes", _E4M3, x.shape, dev)
@@ -226,6 +241,8 @@ def moe_swiglu_fp8(gate_up, codes, scales, live_rows=None, stream=None):
     if W % 2:
         raise ValueError("gate_up: shape %s, expected [rows, 2 * columns]" % (tuple(gate_up.shape),))
     C = W // 2
+    if (R | C) >> 31:
+        _too_large("moe_swiglu_fp8")
     pc = _packed(codes, "codes", _E4M3, (R, C), dev)
     ps = _packed(scales, "scales", _F32, (R, C // 128), dev)
     pl = _packed(live_rows, "live_rows", _I32, (1,), dev)
@@ -247,6 +264,8 @@ def moe_product_fp8(a, a_scales, b, b_scales, out, offsets=None, status=None, st
     if b.dim() != (2 if offsets is None else 3):
         raise ValueError("b: shape %s, expected %s" % (tuple(b.shape), "[N, K]" if offsets is None else "[G, N, K]"))
     N, G = b.shape[-2], lead[0] if lead else 0
+    if (M | K | N | G) >> 31:
+        _too_large("moe_product_fp8")
     pb = _packed(b, "b", _E4M3, (*lead, N, K), dev)
     ps = _packed(a_scales, "a_scales", _F32, (M, K // 128), dev)
     pt = _packed(b_scales, "b_scales", _F32, (*lead, -(-N // 128), K // 128), dev)
