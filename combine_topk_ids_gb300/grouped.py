@@ -107,6 +107,8 @@ def moe_sort_picks(topk_ids, num_experts, offsets, position, workspace, source=N
         _too_large("moe_sort_picks")
     po = _packed(offsets, "offsets", _I32, (num_experts + 1,), dev)
     pp = _packed(position, "position", _I32, (T, k), dev)
+    if workspace is not None:
+        _typed(workspace, "workspace", _BYTE)
     pw = None if workspace is None else _packed(workspace, "workspace", _BYTE, workspace.shape, dev)
     ps = _packed(source, "source", _I32, (T * k,), dev)
     pt = _packed(status, "status", _I32, (1,), dev)
