@@ -259,7 +259,8 @@ def moe_product_fp8(a, a_scales, b, b_scales, out, offsets=None, status=None, st
     (scales [ceil(N / 128), K / 128]), or, with offsets int32 [G + 1] as moe_sort_picks writes them,
     b [G, N, K] (scales [G, ..]) of which rows offsets[g] to offsets[g + 1] take matrix g; rows of no
     group are left as they were.  out [M, N] bf16 or float32.  status: int32 [1], into which
-    MOE_STATUS_TIMEOUT is or-ed where a wait of the kernel gave up."""
+    MOE_STATUS_TIMEOUT is or-ed where a wait of the kernel gave up, and out is not valid; without it that
+    cannot be seen.  The caller clears the word: moe_sort_picks with the same word does."""
     (M, K), dev, pa, sa = _matrix(a, "a", _E4M3)
     _typed(b, "b", _E4M3)
     lead = b.shape[:-2]

@@ -43,11 +43,11 @@ class Ffn:
         self.gate_up, self.act, self.out = empty(rows, 2 * I, dtype=BF), empty(rows, I, dtype=F8), empty(rows, H, dtype=BF)
         self.scales = empty(rows, I // 128)
 
-    def forward(self, codes, scales, offsets=None):
+    def forward(self, codes, scales, status, offsets=None):
         live = None if offsets is None else offsets[-1:]
-        moe.moe_product_fp8(codes, scales, *self.w1, self.gate_up, offsets=offsets)
+        moe.moe_product_fp8(codes, scales, *self.w1, self.gate_up, offsets=offsets, status=status)
         moe.moe_swiglu_fp8(self.gate_up, self.act, self.scales, live_rows=live)
-        moe.moe_product_fp8(self.act, self.scales, *self.w2, self.out, offsets=offsets)
+        moe.moe_product_fp8(self.act, self.scales, *self.w2, self.out, offsets=offsets, status=status)
         return self.out
 
 
@@ -65,18 +65,26 @@ class GroupedBlock:
         self.workspace = empty(moe.moe_sort_picks_workspace_size(T, k, E), dtype=torch.uint8)
         self.rows, self.rows_scales = empty(T * k, H, dtype=F8), empty(T * k, H // 128)
         self.routed = empty(T, H, dtype=BF)
+        self.status = empty(1, dtype=torch.int32)
 
     def forward(self, x, residual):
-        """residual += x; the block's output."""
+        """residual += x; the block's output, which is valid if check() finds nothing.  The order of the picks
+        writes the status word, and the products after it add to it."""
         moe.moe_add_rmsnorm(x, residual, self.norm, EPS, sum_out=residual, out=self.y, out_fp8=self.codes,
                             scales=self.scales)
         self.logits = torch.mm(self.y, self.gate.t()).float()
         moe.moe_route_topk(self.router, self.logits, None, self.ids, self.weights)
-        moe.moe_sort_picks(self.ids, self.E, self.offsets, self.position, self.workspace)
+        moe.moe_sort_picks(self.ids, self.E, self.offsets, self.position, self.workspace, status=self.status)
         moe.moe_sort_rows(self.codes, self.position, self.rows, x_scales=self.scales, rows_scales=self.rows_scales)
-        self.experts.forward(self.rows, self.rows_scales, self.offsets)
+        self.experts.forward(self.rows, self.rows_scales, self.status, self.offsets)
         moe.moe_unsort_rows(self.experts.out, self.weights, self.position, self.routed)
-        return self.routed + self.shared.forward(self.codes, self.scales)
+        return self.routed + self.shared.forward(self.codes, self.scales, self.status)
+
+    def check(self):
+        """Raises where the last forward met a bad expert id or a product's wait gave up (synchronises)."""
+        bits = self.status.item()
+        if bits:
+            raise RuntimeError("the forward is invalid: status 0x%x (moe.STATUS_*)" % bits)
 
     def router_backward(self, dout):
         """d(routing weights) and d(logits) of the last forward, from the output's gradient."""
@@ -106,6 +114,7 @@ def main():
     for tokens in (1, cfg.tokens):
         block, x, residual = make(cfg, tokens)
         out = block.forward(x, residual)
+        block.check()
         dweights, dlogits = block.router_backward(torch.ones_like(out))
         print("%d tokens: |out| %.4f, |dweights| %.4f, |dlogits| %.4f"
               % (tokens, out.float().norm(), dweights.norm(), dlogits.norm()))

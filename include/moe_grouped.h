@@ -143,8 +143,9 @@ typedef struct {
  *                they do not ascend, what out holds afterwards is undefined); rows of no group are left
  *                as they were in out and do not matter in a
  *   out_dev      bf16 or float32 [num_rows, n]; does not overlap the inputs
- *   status_dev   one int32 into which MOE_STATUS_TIMEOUT is or-ed where a wait of the kernel gave
- *                up, or NULL; the caller clears it
+ *   status_dev   one int32 into which MOE_STATUS_TIMEOUT is or-ed where a wait of the kernel gave up, and
+ *                out is then not valid; or NULL, and that cannot be seen.  The caller clears it: one
+ *                word serves a chain of calls, which moe_sort_picks writes and the products add to
  * Products of codes are exact, sums are float32, and so are the scales' products; out is rounded
  * once.  The order of the sums depends on the sizes alone, so equal inputs give equal bits.
  * The gradient of a is the same product on the transposed codes and block scales of b.
