@@ -57,10 +57,12 @@ struct ProductArgs {
     int out_map;                // wide tiles: out has a tensor map (rows on 16-byte boundaries)
 };
 
-// First row of group g, between 0 and M whatever the offsets hold.
+// First row of group g, between 0 and M whatever the offsets hold.  (Offsets and scales are read by plain loads, not
+// through the read-only path: that asks for memory which does not change while the kernel runs, and this one is
+// launched while the kernel that writes them does.  The times are the same.)
 __device__ __forceinline__ int row_of(const ProductArgs &a, int g) {
     if (!a.offsets) return g ? a.M : 0;
-    return min(max(__ldg(a.offsets + g), 0), a.M);
+    return min(max(a.offsets[g], 0), a.M);
 }
 
 // prefix[g] = tiles of `rows` rows in the groups before g, g <= G; the number of tiles.  All threads of the
@@ -337,11 +339,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = k0; k < k1; k += kScaleSteps, ++turn) {
                 float *tab = table + (turn & 1) * (kScaleSteps * NT);   // [8][NT]
                 const bool in = k + (lane & 7) < k1;
-                const float w = in ? __ldg(sb + k) : 0.f;
+                const float w = in ? sb[k] : 0.f;
                 float r[NT / 4];
 #pragma unroll
                 for (int j = 0; j < NT / 4; ++j)
-                    r[j] = in && 4 * j + (lane >> 3) < t.rows ? __ldg(sa + (int64_t)(4 * j) * a.kb + k) : 0.f;
+                    r[j] = in && 4 * j + (lane >> 3) < t.rows ? sa[(int64_t)(4 * j) * a.kb + k] : 0.f;
                 if (!mbar_wait(sempty0 + 8 * (turn & 1), ((turn >> 1) & 1) ^ 1, abort_flag, status)) { ok = false; break; }
 #pragma unroll
                 for (int j = 0; j < NT / 4; ++j) tab[(lane & 7) * NT + 4 * j + (lane >> 3)] = w * r[j];
@@ -630,14 +632,14 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                     const uint32_t b = turn & 1;
                     float *tab = tables + b * (S::kTable / 4);   // [128][8], then [2][8]
                     const bool in = k + (lane & 7) < a.kb;
-                    const float w = in && lane < 16 ? __ldg(sb + k) : 0.f;
+                    const float w = in && lane < 16 ? sb[k] : 0.f;
 #pragma unroll 1
                     for (int h = 0; h < 4; ++h) {
                         float r[8];
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
                             const int at = 4 * (8 * h + j);
-                            r[j] = in && at + (lane >> 3) < rows ? __ldg(sa + (int64_t)at * a.kb + k) : 0.f;
+                            r[j] = in && at + (lane >> 3) < rows ? sa[(int64_t)at * a.kb + k] : 0.f;
                         }
                         if (h == 0 && !mbar_wait(sempty0 + 8 * b, ((turn >> 1) & 1) ^ 1, abort_flag, status)) { ok = false; break; }
 #pragma unroll
