@@ -4,9 +4,11 @@
 //     out[m, n] = sum over blocks b of  sa[m, b] * sb[g, n / 128, b] * (a[m, b] . b[g, n, b])
 //
 // Bounds.  Few rows: the weights' bytes (HBM; 512 rows over 256 matrices of 4096 x 7168, 206 of them
-// with a row, 786 us, 7.7 TB/s), below some 50 MB of them the launch and the latency of one short wave of tiles
-// (one row by 4096 x 7168 7.9 us, 4.3 of them the bytes).  Many rows: the promotion, and close behind it the
-// operands' way into the ring (32768 x 4096 x 7168 689 us, 2.8 PFLOP/s; the products alone 424 us, with
+// with a row, 787 us, 7.7 TB/s), below some 50 MB of them the launch and the latency of one short wave of tiles
+// (one row by 4096 x 7168 7.8 us, 4.3 of them the bytes).  64 to 2048 rows: SMs without a tile, or with one when others
+// have two (512 x 4096 x 7168 34 us: 64 wide tiles, each through all k-steps).  Many rows: the promotion, and
+// close behind it the operands' way into the ring (32768 x 4096 x 7168 688 us in bursts, 2.8 PFLOP/s, and 778, 2.5, in a
+// loop of seconds, where the clock falls to 1.65 to 1.75 GHz; in bursts the products alone 424 us, with
 // their operands 592, with the promotion and no operands 640; the tensor cores are busy in half of the
 // cycles).
 //
@@ -919,18 +921,19 @@ struct Choice {
 // The tiles with the least estimated time.  A tile's k-steps take `step` ns each (measured: a narrow
 // tile's operands at 80 to 90 GB/s for an SM up to 64 rows, its promotion at 128; a wide tile's promotion),
 // what comes before and after them about 1 us (wide: 1.5), sharing a tile 1 to 2 us more (among 8 blocks
-// up to 3).  Several groups' weights come from HBM, 16 KB (wide: 32) for a k-step, and a group of r rows is taken for r / rows + 1/2 row tiles, as the rows of groups of different sizes come to.
-// Measured, us, by tiles of 16, 32, 64 and 128 rows and wide ones:
-//     rows x n x k             1 x 4096 x 7168    7.9   8.6  10.5  14.8   28.8
-//                             64 x 4096 x 7168   14.9  11.5  10.5  13.2   32.4
-//                            128 x 4096 x 7168   26.0  16.3  14.7  14.5   34.5
-//                            512 x 4096 x 7168   80.8  52.5  40.7  34.8   33.6
-//                            777 x 1003 x 1408   11.3  10.5   9.2  11.8   17.8
-//     256 groups, 8 rows each, 4096 x 7168        1068  1079  1093  1676   1146
-//                16 rows                          1145  1098  1106  1699   1156
-//                32 rows                          1594  1217  1172  1743   1175
-//                64 rows                             -     -  1474     -   1242
-// (the groups before the scales had a warp of their own, which brought 2 to 4% to all)
+// up to 3).  Several groups' weights come from HBM, 16 KB (wide: 32) for a k-step, and a group of r rows is
+// taken for r / rows + 1/2 row tiles, as the rows of groups of different sizes come to.
+// Measured, us, by tiles of 16, 32, 64 and 128 rows (with the split that the rule gives them) and wide ones; the
+// rule takes the least of each line, or what is within 0.2% of it:
+//     rows x n x k             1 x 4096 x 7168    7.6   8.4  10.6  14.9   29.4
+//                             64 x 4096 x 7168   14.6  11.7  10.1  12.9   30.7
+//                            128 x 4096 x 7168   25.6  16.1  14.5  14.3   33.6
+//                            512 x 4096 x 7168   80.5  52.6  39.6  34.5   33.4
+//                            777 x 1003 x 1408   11.1  10.3   9.0  11.6   16.8
+//     256 groups, 8 rows each, 4096 x 7168        1061  1077  1085  1503   1135
+//                16 rows                          1129  1095  1097  1514   1143
+//                32 rows                          1547  1179  1134  1538   1155
+//                64 rows                          2769  1678  1442  1711   1213
 Choice choose_tiles(const ProductArgs &p) {
     static const struct { int rows, n, step, around; } kTiles[] = {
         {16, kTileN, 200, 1000}, {32, kTileN, 230, 1000}, {64, kTileN, 320, 1000}, {128, kTileN, 550, 1000}, {0, kWideN, 500, 1500}};

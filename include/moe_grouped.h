@@ -108,11 +108,12 @@ typedef struct {
  *   its block's scale; an infinity makes its whole block NaN.
  * moe_swiglu_fp8 - v = silu(gate) * up of gate_up [matrices, num_rows, 2 * cols] (the gate in the first half
  *   of the columns) in float32, quantised the same way (block_rows 1).  silu(g) = g / (1 + exp(-g)); where
- *   1 / (1 + exp(-g)) is below 2^-126, the smallest normal float32 (finite g below -87.3), silu is 0.  At
+ *   1 / (1 + exp(-g)) is below 2^-126, the smallest normal float32 (finite g below -126 ln 2 = -87.34), silu is 0.  At
  *   g = -infinity the formula is not a number, which marks that column's code alone.
  * live_rows_dev: one int32 in device memory, or NULL: only the first that many rows are taken,
  *   the outputs of those behind are left as they were (with moe_sort_picks: &offsets[num_experts]).
  *   It has to be NULL with block_rows 128 or several matrices.
+ * The outputs do not overlap the inputs.
  * Errors: MOE_ERR_INVALID_ARGUMENT, MOE_ERR_HIDDEN_ALIGNMENT (cols % 128 != 0), MOE_ERR_LIMIT
  * (cols above MOE_MAX_HIDDEN), MOE_ERR_MISALIGNED (codes off 16 bytes, others off their element).
  */
