@@ -63,4 +63,5 @@ def test_infinite_gates_and_nan(dtype):
     for v, rel, codes, scales in (low, nan):
         assert np.isnan(codes[0, 0]) and np.isfinite(codes[0, 1:]).all()
         within(codes[0, 1:] * scales[0], v[0, 1:], (E4M3 + 2 * rel) * np.abs(v[0, 1:]) + 2.0 ** -10 * 1.001 * scales[0], "beside")
-    assert np.isnan(high[2] * high[3]).all()
+    with np.errstate(invalid="ignore"):      # codes of 0 by an infinite scale
+        assert np.isnan(high[2] * high[3]).all()
